@@ -51,7 +51,8 @@ enum {
   GPT2_ERR_BATCH = -5,        /* B > B_max, B differs between accumulated micro-batches, or B*T too large */
   GPT2_ERR_NO_GRAD = -6,      /* gpt2_step / gpt2_get_grads with no accumulated micro-batch */
   GPT2_ERR_CUDA = -7,         /* a CUDA runtime or driver call failed */
-  GPT2_ERR_TIMEOUT = -8       /* a bounded device-side wait gave up */
+  GPT2_ERR_TIMEOUT = -8,      /* a bounded device-side wait gave up */
+  GPT2_ERR_PAGE_RANGE = -9    /* a page id, sequence, position or length outside a paged cache */
 };
 
 enum { GPT2_FP32 = 0, GPT2_BF16 = 1 };
@@ -422,6 +423,79 @@ int gpt2_op_gemv(const void* x, int64_t ldx, int B, const void* W, int N, int K,
  * arguments, all DEVICE pointers). Synchronises. */
 int gpt2_op_sample_topk(const float* logits, int64_t ld, int rows, int V, int k, float temperature, float top_p,
                         const double* u, int32_t* idx_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key/value cache (no counterpart on the pages: the cache of gpt2_prefill /
+ * gpt2_decode_step holds sequences of one common length; these calls serve sequences of
+ * different lengths from one pool of pages). Caller-owned DEVICE memory, asynchronous on
+ * `stream`; nothing is allocated, so the calls can be captured into a CUDA graph (make the
+ * first call of each kind on a device before the capture: it sets kernel attributes).
+ *
+ * k, v: element (page 0, token slot 0, head 0) of the two pools. Slot s of page p holds, for
+ * key head h, head_dim contiguous elements at p*page_stride + s*row_stride + h*head_stride
+ * (in elements, the same for k and v; any order of the three). page_table: int32 [n_seqs]
+ * [max_pages], row stride table_stride: position t of sequence b is in page
+ * page_table[b*table_stride + t / page_size], slot t % page_size; entries behind a sequence's
+ * last page are not read. dtype: GPT2_BF16 or GPT2_FP32, of the pools, keys, values, queries
+ * and outputs. head_dim 32, 64, 96 or 128; page_size a power of two, at most 4096; at most
+ * 4096 sequences and 2^30 tokens each; k, v and the strides multiples of 16 bytes
+ * (GPT2_ERR_CONFIG, _BATCH or _SEQ_TOO_LONG otherwise, before anything is launched).
+ * status (nullable): int32 device word, zero at first. Contents of device memory cannot be
+ * checked by the host: a page id outside [0, n_pages), a sequence, position or length outside
+ * the cache is not followed, the access is skipped as documented at each call, and the word
+ * is raised; gpt2_op_paged_status reports it.
+ * The struct is read during the call only. */
+typedef struct {
+  void *k, *v;
+  int64_t page_stride, row_stride, head_stride;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int32_t* status;
+  int32_t dtype, n_pages, page_size, max_pages, n_seqs, n_kv_heads, head_dim;
+} gpt2_paged_kv;
+
+/* Append the keys and values of N new tokens. Row n (n_kv_heads heads of head_dim contiguous
+ * elements at k + n*ldk and v + n*ldv) goes to position positions[n] of sequence seqs[n]
+ * (seqs NULL: sequence n, N <= n_seqs). positions[n] < 0 marks a padding row: it is skipped.
+ * With rot_dim > 0 (a multiple of 16, at most head_dim) the keys are rotated on the way by
+ * the table f32_cos_sin [n_positions][rot_dim] (16-byte aligned; row t: the rot_dim/2 cosines,
+ * then the sines, of position t): the pair (x, y) of elements (i, i + rot_dim/2), or (2i,
+ * 2i + 1) when interleaved != 0, becomes (x c_i - y s_i, x s_i + y c_i), computed in fp32 and
+ * rounded once; elements from rot_dim on are copied. q (nullable, with q_out and n_q_heads):
+ * query rows of the same tokens, rotated the same way into q_out (may be q itself, with the
+ * same row stride). A row whose position, sequence, table entry or rotation row is outside
+ * its range is skipped and raises the status word; rows that are skipped leave q_out as it
+ * was. Rows must name distinct slots: of two rows for one slot, each 16 bytes come from
+ * either. Row bases and strides are multiples of 16 bytes. */
+int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                            const void* q, int64_t ldq, void* q_out, int64_t ldqo, int n_q_heads, int N,
+                            const int32_t* positions, const int32_t* seqs, const float* f32_cos_sin, int n_positions,
+                            int rot_dim, int interleaved, void* stream);
+
+/* Attention of one new token per sequence over the cache: for each sequence b with L =
+ * seq_lens[b] cached tokens (the new one, already appended, is the last) and each query head
+ * h of n_q_heads (a multiple of n_kv_heads; head h reads key head h / (n_q_heads /
+ * n_kv_heads)): out = sum_t softmax_t(scale q.k_t) v_t over the visible positions t, which
+ * are all t < L (window 0) or the newest `window` and the first `sinks` of them (window > 0).
+ * q and out: rows of n_q_heads heads of head_dim contiguous elements, row strides ldq and ldo;
+ * f32_lse (nullable): [n_seqs][n_q_heads], the natural logarithm of the sum of exponentials.
+ * L = 0 gives out = 0 and lse = -inf. A length outside [0, max_pages*page_size] is brought to
+ * the nearer end, a key whose page id is bad is left out, and both raise the status word.
+ * Softmax statistics and sums are fp32, each output is rounded once. out may not overlap q,
+ * the cache or ws. ws: DEVICE workspace of gpt2_paged_attention_ws_bytes bytes, 16-byte
+ * aligned, of any content; calls that may run at the same time need one each.
+ * Deterministic for given lengths. */
+int gpt2_op_paged_attention(const gpt2_paged_kv* kv, const void* q, int64_t ldq, int n_q_heads,
+                            const int32_t* seq_lens, float scale, int window, int sinks, void* out, int64_t ldo,
+                            float* f32_lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of gpt2_op_paged_attention's workspace (0 for sizes it refuses). */
+size_t gpt2_paged_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim);
+
+/* Wait for `stream`, read and clear the cache's status word: GPT2_ERR_PAGE_RANGE if a call on
+ * the cache met a bad page id, sequence, position or length since it was last cleared.
+ * GPT2_ERR_CONFIG for a cache without one. */
+int gpt2_op_paged_status(const gpt2_paged_kv* kv, void* stream);
 
 /* Check of the device-side timeout path (no counterpart on the pages: it tests the
  * library's error reporting). One thread initialises an mbarrier of count 1,

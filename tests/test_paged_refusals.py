@@ -1,0 +1,162 @@
+"""The paged cache calls refuse what they cannot do before anything is launched, and the
+index arithmetic they share with the kernels is checked exhaustively (CPU only)."""
+import ctypes as ct
+import os
+import subprocess
+
+import pytest
+
+import train_step_b200 as tsb
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+A = 0x7F0000001000  # an address that is never read: every call below is refused on the host
+
+CONFIG, TOO_LONG, BATCH = -1, -3, -5
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from train_step_b200 import build
+    build.build()
+
+
+def cache(**kw):
+    f = dict(k=A, v=A, page_stride=16 * 2 * 64, row_stride=2 * 64, head_stride=64, page_table=A, table_stride=8,
+             status=None, dtype=tsb.BF16, n_pages=100, page_size=16, max_pages=8, n_seqs=3, n_kv_heads=2, head_dim=64)
+    f.update(kw)
+    return tsb._PagedKV(**f)
+
+
+def append(kv, **kw):
+    f = dict(k=A, ldk=128, v=A, ldv=128, q=A, ldq=256, q_out=A, ldqo=256, nh=4, N=3, positions=A, seqs=A, cos_sin=A,
+             n_positions=128, rot=64, pairs=0)
+    f.update(kw)
+    return tsb.lib().gpt2_op_paged_kv_append(kv if kv is None else ct.byref(kv), f["k"], f["ldk"], f["v"], f["ldv"],
+                                             f["q"], f["ldq"], f["q_out"], f["ldqo"], f["nh"], f["N"], f["positions"],
+                                             f["seqs"], f["cos_sin"], f["n_positions"], f["rot"], f["pairs"], None)
+
+
+def attend(kv, **kw):
+    f = dict(q=A, ldq=256, nh=4, lens=A, scale=0.125, window=0, sinks=0, out=A, ldo=256, lse=A, ws=A, ws_bytes=1 << 40)
+    f.update(kw)
+    return tsb.lib().gpt2_op_paged_attention(kv if kv is None else ct.byref(kv), f["q"], f["ldq"], f["nh"], f["lens"],
+                                             f["scale"], f["window"], f["sinks"], f["out"], f["ldo"], f["lse"],
+                                             f["ws"], f["ws_bytes"], None)
+
+
+BAD_CACHES = [
+    (dict(k=None), CONFIG), (dict(v=None), CONFIG), (dict(page_table=None), CONFIG), (dict(k=A + 8), CONFIG),
+    (dict(v=A + 2), CONFIG), (dict(page_table=A + 2), CONFIG), (dict(status=A + 1), CONFIG), (dict(dtype=7), CONFIG),
+    (dict(head_dim=48), CONFIG), (dict(head_dim=0), CONFIG), (dict(head_dim=256), CONFIG), (dict(n_pages=0), CONFIG),
+    (dict(max_pages=0), CONFIG), (dict(n_kv_heads=0), CONFIG), (dict(n_kv_heads=2048), CONFIG),
+    (dict(n_seqs=-1), CONFIG), (dict(n_seqs=4097), BATCH), (dict(page_size=24), CONFIG), (dict(page_size=0), CONFIG),
+    (dict(page_size=8192), CONFIG), (dict(table_stride=7), CONFIG), (dict(page_stride=2052), CONFIG),
+    (dict(row_stride=-128), CONFIG), (dict(head_stride=4), CONFIG),
+    (dict(max_pages=1 << 20, table_stride=1 << 20, page_size=2048), TOO_LONG),
+]
+
+
+@pytest.mark.parametrize("change,code", BAD_CACHES)
+def test_a_bad_cache_is_refused_by_both_calls(change, code):
+    assert append(cache(**change)) == code
+    assert attend(cache(**change)) == code
+    assert b"paged cache" in tsb.lib().gpt2_op_last_error()
+
+
+def test_a_null_cache_is_refused():
+    assert append(None) == CONFIG and attend(None) == CONFIG
+    assert tsb.lib().gpt2_op_paged_status(None, None) == CONFIG
+    assert tsb.lib().gpt2_op_paged_status(ct.byref(cache()), None) == CONFIG  # no status word
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(k=None), CONFIG), (dict(v=None), CONFIG), (dict(k=A + 8), CONFIG), (dict(ldk=120), CONFIG),
+    (dict(ldv=132), CONFIG), (dict(q=None), CONFIG), (dict(q_out=None), CONFIG), (dict(nh=0), CONFIG),
+    (dict(nh=-1), CONFIG), (dict(nh=5000, ldq=320000, ldqo=320000), CONFIG), (dict(ldq=248), CONFIG),
+    (dict(ldqo=260), CONFIG), (dict(q_out=A + 4), CONFIG), (dict(N=-1), CONFIG), (dict(positions=None), CONFIG),
+    (dict(seqs=None, N=4), BATCH), (dict(rot=8), CONFIG), (dict(rot=80), CONFIG), (dict(rot=-16), CONFIG),
+    (dict(cos_sin=None), CONFIG), (dict(cos_sin=A + 4), CONFIG), (dict(n_positions=0), CONFIG),
+])
+def test_append_refuses(change, code):
+    assert append(cache(), **change) == code
+    assert b"paged_kv_append" in tsb.lib().gpt2_op_last_error()
+
+
+def test_append_of_no_rows_does_nothing():
+    assert append(cache(), N=0) == 0
+    assert append(cache(), N=0, positions=None) == 0
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(q=None), CONFIG), (dict(out=None), CONFIG), (dict(q=A + 8), CONFIG), (dict(ldq=248), CONFIG),
+    (dict(ldo=252), CONFIG), (dict(nh=0), CONFIG), (dict(nh=3), CONFIG), (dict(nh=4098), CONFIG),
+    (dict(lens=None), CONFIG), (dict(scale=0.0), CONFIG), (dict(scale=-1.0), CONFIG),
+    (dict(scale=float("nan")), CONFIG), (dict(scale=float("inf")), CONFIG), (dict(window=-1), CONFIG),
+    (dict(sinks=-1), CONFIG), (dict(ws=None), CONFIG), (dict(ws=A + 8), CONFIG), (dict(ws_bytes=0), CONFIG),
+])
+def test_attention_refuses(change, code):
+    assert attend(cache(), **change) == code
+    assert b"paged_attention" in tsb.lib().gpt2_op_last_error()
+
+
+def test_attention_of_no_sequences_does_nothing():
+    assert attend(cache(n_seqs=0)) == 0
+
+
+def test_workspace_size():
+    f = tsb.lib().gpt2_paged_attention_ws_bytes
+    assert f(3, 4, 2, 64) > 0 and f(0, 4, 2, 64) > 0 and f(4096, 128, 1, 128) > 0
+    for bad in ((-1, 4, 2, 64), (4097, 4, 2, 64), (3, 5, 2, 64), (3, 0, 2, 64), (3, 4, 0, 64), (3, 4, 2, 0)):
+        assert f(*bad) == 0
+
+
+INDEX_CHECK = r"""
+#include <cstdio>
+#include <set>
+#include "paged_index.cuh"
+using namespace g2;
+int main() {
+  for (int len = 0; len < 40; ++len)
+    for (int window = 0; window < 45; ++window)
+      for (int sinks = 0; sinks < 45; ++sinks) {
+        std::set<int> want, got;
+        for (int j = 0; j < len; ++j)
+          if (window == 0 || j >= len - window || j < sinks) want.insert(j);
+        const PagedVisible v = paged_visible(len, window, sinks);
+        int last = -1;
+        for (int i = 0; i < v.count; ++i) {
+          const int p = paged_position(v, i);
+          if (p <= last) return 1;
+          last = p;
+          got.insert(p);
+        }
+        if (got != want) return 2;
+      }
+  // the extremes do not overflow
+  const int big = 1 << 30, most = 0x7fffffff;
+  if (paged_visible(big, most, most).count != big || paged_visible(big, 1, most).count != big) return 3;
+  if (paged_visible(big, 1, 0).count != 1 || paged_position(paged_visible(big, 1, 0), 0) != big - 1) return 4;
+  int bad = 0;
+  if (paged_length(5, 10, &bad) != 5 || paged_length(10, 10, &bad) != 10 || bad) return 5;
+  if (paged_length(11, 10, &bad) != 10 || !bad) return 6;
+  bad = 0;
+  if (paged_length(-3, 10, &bad) != 0 || !bad) return 7;
+  return 0;
+}
+"""
+
+
+def test_index_arithmetic(tmp_path):
+    src = tmp_path / "check.cpp"
+    src.write_text(INDEX_CHECK)
+    exe = tmp_path / "check"
+    subprocess.run(["g++", "-O1", "-std=c++17", "-x", "c++", "-I" + os.path.join(ROOT, "train_step_b200", "csrc"),
+                    str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_binding_refuses_what_is_not_on_a_gpu():
+    import torch
+    k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        tsb.PagedKV(k, k.clone(), torch.zeros(2, 2, dtype=torch.int32))

@@ -21,6 +21,7 @@ EPI_BIAS, EPI_BIAS_GELU, EPI_RESID, EPI_DGELU, EPI_F32 = 0, 1, 2, 3, 4
 ERRORS = {
     -1: "GPT2_ERR_CONFIG", -2: "GPT2_ERR_OOM", -3: "GPT2_ERR_SEQ_TOO_LONG", -4: "GPT2_ERR_TOKEN_RANGE",
     -5: "GPT2_ERR_BATCH", -6: "GPT2_ERR_NO_GRAD", -7: "GPT2_ERR_CUDA", -8: "GPT2_ERR_TIMEOUT",
+    -9: "GPT2_ERR_PAGE_RANGE",
 }
 
 
@@ -32,6 +33,13 @@ class Gpt2Error(RuntimeError):
 
 class _Config(ct.Structure):
     _fields_ = [(n, ct.c_int) for n in ("L", "H", "C", "T", "V", "tied", "qkv_bias", "dtype", "B_max")]
+
+
+class _PagedKV(ct.Structure):
+    _fields_ = [("k", ct.c_void_p), ("v", ct.c_void_p), ("page_stride", ct.c_int64), ("row_stride", ct.c_int64),
+                ("head_stride", ct.c_int64), ("page_table", ct.c_void_p), ("table_stride", ct.c_int64),
+                ("status", ct.c_void_p)] + [(n, ct.c_int32) for n in (
+                    "dtype", "n_pages", "page_size", "max_pages", "n_seqs", "n_kv_heads", "head_dim")]
 
 
 _lib = None
@@ -107,6 +115,14 @@ _SYMBOLS = {
                              ct.POINTER(ct.c_int64), ct.POINTER(ct.c_int), ct.POINTER(ct.c_int64)], ct.c_int),
     "gpt2_set_grad_events": ([ct.c_void_p, ct.POINTER(ct.c_void_p), ct.c_int], ct.c_int),
     "gpt2_read_loss": ([ct.c_void_p, ct.POINTER(ct.c_float)], ct.c_int),
+    "gpt2_op_paged_kv_append": ([ct.POINTER(_PagedKV), ct.c_void_p, ct.c_int64, ct.c_void_p, ct.c_int64, ct.c_void_p,
+                                 ct.c_int64, ct.c_void_p, ct.c_int64, ct.c_int, ct.c_int, ct.c_void_p, ct.c_void_p,
+                                 ct.c_void_p, ct.c_int, ct.c_int, ct.c_int, ct.c_void_p], ct.c_int),
+    "gpt2_op_paged_attention": ([ct.POINTER(_PagedKV), ct.c_void_p, ct.c_int64, ct.c_int, ct.c_void_p, ct.c_float,
+                                 ct.c_int, ct.c_int, ct.c_void_p, ct.c_int64, ct.c_void_p, ct.c_void_p, ct.c_size_t,
+                                 ct.c_void_p], ct.c_int),
+    "gpt2_paged_attention_ws_bytes": ([ct.c_int, ct.c_int, ct.c_int, ct.c_int], ct.c_size_t),
+    "gpt2_op_paged_status": ([ct.POINTER(_PagedKV), ct.c_void_p], ct.c_int),
     "gpt2_op_last_error": ([], ct.c_char_p),
 }
 
@@ -579,6 +595,161 @@ def cross_entropy(logits, V, targets, scale, row_loss, stream=None):
     N, ld = logits.shape
     _op(lib().gpt2_op_cross_entropy(_dt(logits), _ptr(logits), ld, N, V, _ptr(targets), scale, _ptr(row_loss),
                                     _stream(stream)))
+
+
+class PagedKV:
+    """A paged key/value cache on caller-owned CUDA tensors (see gpt2_paged_kv).
+
+    k_cache, v_cache: [n_pages, page_size, n_kv_heads, head_dim] bf16 or fp32, the same shape
+    and strides, elements of a head contiguous; a permuted view of pages stored in another
+    order (say [n_pages, n_kv_heads, page_size, head_dim].transpose(1, 2)) is as good.
+    page_table: int32 [n_seqs, max_pages]. The tensors are used in place: entries may change
+    between calls, the tensors themselves are kept alive by this object. The calls run on
+    torch's current stream of the tensors' device."""
+
+    def __init__(self, k_cache, v_cache, page_table):
+        import torch
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if t.dim() != 4 or t.dtype not in (torch.bfloat16, torch.float32) or not t.is_cuda:
+                raise ValueError(f"{name} must be a bf16 or fp32 CUDA tensor "
+                                 "[n_pages, page_size, n_kv_heads, head_dim]")
+        if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride() or k_cache.dtype != v_cache.dtype:
+            raise ValueError("k_cache and v_cache must have the same type, shape and strides")
+        if k_cache.stride(3) != 1:
+            raise ValueError("the elements of a head must be contiguous")
+        if page_table.dim() != 2 or page_table.dtype != torch.int32 or (page_table.shape[1] > 1
+                                                                        and page_table.stride(1) != 1):
+            raise ValueError("page_table must be an int32 tensor [n_seqs, max_pages] with contiguous rows")
+        if not (k_cache.device == v_cache.device == page_table.device):
+            raise ValueError("k_cache, v_cache and page_table must be on one device")
+        self.k_cache, self.v_cache, self.page_table = k_cache, v_cache, page_table
+        self.device, self.dtype = k_cache.device, k_cache.dtype
+        n_pages, page_size, self.n_kv_heads, self.head_dim = k_cache.shape
+        self.n_seqs, max_pages = page_table.shape
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        ps, rs, hs, _ = k_cache.stride()
+        # a table of one row may have any stride, and so may a dimension of one element
+        ts = page_table.stride(0) if self.n_seqs > 1 else max_pages
+        self._c = _PagedKV(_ptr(k_cache), _ptr(v_cache), ps if n_pages > 1 else 0, rs if page_size > 1 else 0,
+                           hs if self.n_kv_heads > 1 else 0, _ptr(page_table), ts, _ptr(self.status), _dt(k_cache),
+                           n_pages, page_size, max_pages, self.n_seqs, self.n_kv_heads, self.head_dim)
+        self._ref = ct.byref(self._c)
+
+    def attention_workspace(self, n_heads: int):
+        """A workspace for paged_attention with n_heads query heads (one per concurrent call)."""
+        import torch
+        n = lib().gpt2_paged_attention_ws_bytes(self.n_seqs, n_heads, self.n_kv_heads, self.head_dim)
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def check(self, stream=None) -> None:
+        """Wait for the stream and raise Gpt2Error(GPT2_ERR_PAGE_RANGE) if a call on this cache
+        met a bad page id, sequence, position or length since the last check."""
+        with _device_of(self.device):
+            _op(lib().gpt2_op_paged_status(self._ref, _stream(stream)))
+
+    def _rows(self, name, t, n_heads=None):
+        """[N, heads, head_dim] rows of the cache's type and device: their row stride."""
+        if (t.dim() != 3 or t.dtype != self.dtype or t.device != self.device or t.shape[2] != self.head_dim
+                or (n_heads is not None and t.shape[1] != n_heads)):
+            raise ValueError(f"{name} must be [N, {n_heads or 'heads'}, {self.head_dim}] {self.dtype} on {self.device}")
+        N, H, D = t.shape
+        st = t.stride()
+        if st[2] != 1 or (H > 1 and st[1] != D):
+            raise ValueError(f"{name}: the heads of a row must be contiguous")
+        return st[0] if N > 1 else H * D
+
+    def _ints(self, name, t, n):
+        import torch
+        if t.dtype != torch.int32 or t.shape != (n,) or t.device != self.device or (n > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {self.device}")
+
+
+class _NoContext:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *a):
+        pass
+
+
+_NO_CONTEXT = _NoContext()
+
+
+def _device_of(device):
+    """Makes `device` current for a call when it is not."""
+    import torch
+    return _NO_CONTEXT if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def paged_kv_append(cache: PagedKV, k, v, positions, seqs=None, q=None, q_out=None, cos_sin=None,
+                    interleaved: bool = False, stream=None) -> None:
+    """Append the keys and values of N tokens, k and v [N, n_kv_heads, head_dim], at
+    positions[n] (int32; negative: a padding row) of sequence seqs[n] (int32; None: n). With
+    cos_sin (fp32 [n_positions, rot_dim], see rotation_table) keys are rotated on the way, and
+    q [N, n_heads, head_dim] is rotated into q_out (may be q). See gpt2_op_paged_kv_append."""
+    import torch
+    N = k.shape[0]
+    ldk, ldv = cache._rows("k", k, cache.n_kv_heads), cache._rows("v", v, cache.n_kv_heads)
+    cache._ints("positions", positions, N)
+    if seqs is not None:
+        cache._ints("seqs", seqs, N)
+    nh = ldq = ldqo = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        nh = q.shape[1] if q.dim() == 3 else 0
+        ldq, ldqo = cache._rows("q", q, nh), cache._rows("q_out", q_out, nh)
+        if q.shape[0] != N or q_out.shape[0] != N:
+            raise ValueError("q and q_out must have a row per token")
+    if v.shape[0] != N:
+        raise ValueError("k and v must have a row per token")
+    n_pos = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != cache.device                 or not cos_sin.is_contiguous():
+            raise ValueError(f"cos_sin must be a contiguous fp32 tensor [n_positions, rot_dim] on {cache.device}")
+        n_pos, rot = cos_sin.shape
+    with _device_of(cache.device):
+        _op(lib().gpt2_op_paged_kv_append(cache._ref, _ptr(k), ldk, _ptr(v), ldv, _ptr(q), ldq, _ptr(q_out), ldqo, nh,
+                                          N, _ptr(positions), _ptr(seqs), _ptr(cos_sin), n_pos, rot,
+                                          int(interleaved), _stream(stream)))
+
+
+def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None, window: int = 0, sinks: int = 0,
+                    lse=None, ws=None, stream=None) -> None:
+    """Attention of one new token per sequence, q [n_seqs, n_heads, head_dim], over the first
+    seq_lens[b] (int32) cached tokens of each sequence into out (as q): all of them, or the
+    newest `window` and the first `sinks`. lse: optional fp32 [n_seqs, n_heads]. scale: 1 /
+    sqrt(head_dim) by default. ws: cache.attention_workspace(n_heads), to be kept between calls
+    (None: allocated for this one). See gpt2_op_paged_attention."""
+    import torch
+    nh = q.shape[1] if q.dim() == 3 else 0
+    ldq, ldo = cache._rows("q", q, nh), cache._rows("out", out, nh)
+    if q.shape[0] != cache.n_seqs or out.shape[0] != cache.n_seqs:
+        raise ValueError(f"q and out must have a row per sequence ({cache.n_seqs})")
+    cache._ints("seq_lens", seq_lens, cache.n_seqs)
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (cache.n_seqs, nh) or not lse.is_contiguous()
+                            or lse.device != cache.device):
+        raise ValueError(f"lse must be a contiguous fp32 tensor [{cache.n_seqs}, {nh}] on {cache.device}")
+    with _device_of(cache.device):
+        if ws is None:
+            if stream is not None:
+                raise ValueError("a call on an explicit stream needs its own workspace")
+            ws = cache.attention_workspace(nh)
+        elif ws.device != cache.device:
+            raise ValueError(f"ws must be on {cache.device}")
+        _op(lib().gpt2_op_paged_attention(cache._ref, _ptr(q), ldq, nh, _ptr(seq_lens),
+                                          cache.head_dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out),
+                                          ldo, _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def rotation_table(n_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
+    """cos_sin for paged_kv_append: fp32 [n_positions, rot_dim], row t the cosines and then the
+    sines of t * base^(-2i / rot_dim), i < rot_dim / 2, computed in float64 (angles of far
+    positions lose their fraction in 32 bits) and rounded once."""
+    import torch
+    half = rot_dim // 2
+    angle = np.arange(n_positions)[:, None] * float(base) ** (-np.arange(half) / max(1, half))[None, :]
+    return torch.from_numpy(np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)).to(device)
 
 
 def bounded_wait_check(arrive: bool, limit_ns: int, stream=None) -> None:

@@ -14,6 +14,7 @@ enum DeviceError : int {
   DEV_OK = 0,
   DEV_TOKEN_RANGE = 1,   // a token or target id outside [0, V)
   DEV_TIMEOUT = 2,       // a bounded wait on an mbarrier gave up
+  DEV_PAGE_RANGE = 3,    // a page id, sequence, position or length outside the paged cache
 };
 
 __device__ __forceinline__ void raise_device_error(int* err, int code) {

@@ -23,6 +23,7 @@
 #include "gemm_simt.cuh"
 #include "gemm_tc.cuh"
 #include "layernorm.cuh"
+#include "paged.cuh"
 #include "sample.cuh"
 
 namespace g2 {
@@ -1133,6 +1134,123 @@ inline int sample_topk(const LaunchCtx& c, const float* logits, int64_t ld, int 
   ProfScope ps(c, CAT_SAMPLE, 0.0, 5.0 * 4 * rows * V);
   sample_topk_kernel<<<rows, TOPK_THREADS, 0, c.stream>>>(logits, ld, V, k, temperature, top_p, u, out);
   return check_launch(c, "sample_topk");
+}
+
+// ---------------------------------------------------------------------------
+// paged key/value cache
+// ---------------------------------------------------------------------------
+constexpr int PAGED_MAX_SEQS = 4096;
+
+// Checks a caller's cache description and fills the kernels' view of it.
+inline int paged_view(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedView* out) {
+  if (!kv || !kv->k || !kv->v || !kv->page_table)
+    return fail(c, GPT2_ERR_CONFIG, "paged cache: k, v and page_table are required");
+  if (kv->dtype != GPT2_BF16 && kv->dtype != GPT2_FP32)
+    return fail(c, GPT2_ERR_CONFIG, "paged cache: dtype must be GPT2_FP32 or GPT2_BF16");
+  if (kv->head_dim != 32 && kv->head_dim != 64 && kv->head_dim != 96 && kv->head_dim != 128)
+    return fail(c, GPT2_ERR_CONFIG, "paged cache: head_dim must be 32, 64, 96 or 128");
+  if (kv->n_pages < 1 || kv->max_pages < 1 || kv->n_kv_heads < 1 || kv->n_seqs < 0 || kv->table_stride < kv->max_pages)
+    return fail(c, GPT2_ERR_CONFIG,
+                "paged cache: n_pages, max_pages, n_kv_heads >= 1, n_seqs >= 0, table_stride >= max_pages");
+  if (kv->n_kv_heads > 1024) return fail(c, GPT2_ERR_CONFIG, "paged cache: at most 1024 key heads");
+  if (kv->n_seqs > PAGED_MAX_SEQS) return fail(c, GPT2_ERR_BATCH, "paged cache: at most 4096 sequences");
+  if (kv->page_size < 1 || kv->page_size > 4096 || (kv->page_size & (kv->page_size - 1)))
+    return fail(c, GPT2_ERR_CONFIG, "paged cache: page_size must be a power of two, at most 4096");
+  if ((int64_t)kv->max_pages * kv->page_size > (1 << 30))
+    return fail(c, GPT2_ERR_SEQ_TOO_LONG, "paged cache: more than 2^30 tokens per sequence");
+  const int64_t vn = kv->dtype == GPT2_BF16 ? 8 : 4;  // elements of 16 bytes
+  if (kv->page_stride < 0 || kv->row_stride < 0 || kv->head_stride < 0 || kv->page_stride % vn || kv->row_stride % vn ||
+      kv->head_stride % vn || ((reinterpret_cast<uintptr_t>(kv->k) | reinterpret_cast<uintptr_t>(kv->v)) & 15))
+    return fail(c, GPT2_ERR_CONFIG, "paged cache: k, v and the strides must be multiples of 16 bytes");
+  if ((reinterpret_cast<uintptr_t>(kv->page_table) | reinterpret_cast<uintptr_t>(kv->status)) & 3)
+    return fail(c, GPT2_ERR_CONFIG, "paged cache: page_table and status must be 4-byte aligned");
+  int lg = 0;
+  while ((1 << lg) < kv->page_size) ++lg;
+  *out = PagedView{kv->k,      kv->v,      kv->page_stride, kv->row_stride, kv->head_stride,
+                   kv->page_table, kv->table_stride, kv->status, kv->n_pages, lg,
+                   kv->max_pages, kv->n_seqs, kv->n_kv_heads, kv->head_dim};
+  return GPT2_OK;
+}
+
+// rows of `heads` heads: base and row stride on 16 bytes, rows that do not overlap
+inline bool paged_rows_ok(const void* p, int64_t ld, int64_t heads, int hd, int64_t vn) {
+  return p && !(reinterpret_cast<uintptr_t>(p) & 15) && ld % vn == 0 && ld >= heads * hd;
+}
+
+inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedAppendArgs a, bool pairs) {
+  int r = paged_view(c, kv, &a.c);
+  if (r) return r;
+  if (a.rows < 0 || a.nh < 0) return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: negative size");
+  if (a.rows == 0) return GPT2_OK;
+  if (!a.positions) return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: positions are required");
+  if (a.nh > 4096) return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: at most 4096 query heads");
+  if (!a.seqs && a.rows > kv->n_seqs)
+    return fail(c, GPT2_ERR_BATCH, "paged_kv_append: more rows than sequences (and no sequence indices)");
+  const int vn = kv->dtype == GPT2_BF16 ? 8 : 4, hd = kv->head_dim;
+  if ((a.q != nullptr) != (a.nh > 0) || (a.q_out != nullptr) != (a.nh > 0))
+    return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: q, q_out and n_q_heads go together");
+  if (!paged_rows_ok(a.k, a.ldk, a.c.nkv, hd, vn) || !paged_rows_ok(a.v, a.ldv, a.c.nkv, hd, vn) ||
+      (a.nh && (!paged_rows_ok(a.q, a.ldq, a.nh, hd, vn) || !paged_rows_ok(a.q_out, a.ldqo, a.nh, hd, vn))))
+    return fail(c, GPT2_ERR_CONFIG,
+                "paged_kv_append: k, v, q and q_out must start and step on 16 bytes, with row strides of at least a row");
+  if (a.rot < 0 || a.rot > hd || a.rot % 16)
+    return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: rot_dim must be a multiple of 16, at most head_dim");
+  if (a.rot && (!a.cos_sin || a.n_positions < 1 || (reinterpret_cast<uintptr_t>(a.cos_sin) & 15)))
+    return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: a rotation needs a 16-byte aligned cos_sin table");
+  a.tasks_per_row = (a.nh + 2 * a.c.nkv) * (hd / (2 * vn));
+  // four tasks per thread, in rows of at most PKV_MAX_ROWS per block, as long as that leaves
+  // two blocks per SM; otherwise fewer rows and a row's tasks over several blocks
+  a.rows_per_block = std::max(1, std::min(PKV_MAX_ROWS, 4 * PKV_THREADS / a.tasks_per_row));
+  while (a.rows_per_block > 1 && (a.rows + a.rows_per_block - 1) / a.rows_per_block < 2 * c.num_sms)
+    a.rows_per_block /= 2;
+  const dim3 grid((a.rows + a.rows_per_block - 1) / a.rows_per_block,
+                  std::max(1, (a.rows_per_block * a.tasks_per_row + 4 * PKV_THREADS - 1) / (4 * PKV_THREADS)));
+  const bool bf = kv->dtype == GPT2_BF16;
+  auto kern = bf ? (pairs ? paged_append_kernel<bf16, true> : paged_append_kernel<bf16, false>)
+                 : (pairs ? paged_append_kernel<float, true> : paged_append_kernel<float, false>);
+  kern<<<grid, PKV_THREADS, 0, c.stream>>>(a);
+  return check_launch(c, "paged_kv_append");
+}
+
+inline bool paged_heads_ok(int nh, int nkv) { return nkv >= 1 && nh >= 1 && nh <= 4096 && nh % nkv == 0; }
+
+inline size_t paged_attention_ws_bytes(int n_seqs, int nh, int nkv, int hd) {
+  if (n_seqs < 0 || n_seqs > PAGED_MAX_SEQS || !paged_heads_ok(nh, nkv) || hd < 1) return 0;
+  return 16;
+}
+
+inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedAttnArgs a, void* ws, size_t ws_bytes) {
+  int r = paged_view(c, kv, &a.c);
+  if (r) return r;
+  if (!paged_heads_ok(a.nh, a.c.nkv))
+    return fail(c, GPT2_ERR_CONFIG, "paged_attention: n_q_heads must be a multiple of n_kv_heads, at most 4096");
+  if (!(a.scale > 0.f) || a.scale > 3.4e38f || a.window < 0 || a.sinks < 0)
+    return fail(c, GPT2_ERR_CONFIG, "paged_attention: finite scale > 0, window >= 0, sinks >= 0");
+  if (kv->n_seqs == 0) return GPT2_OK;
+  if (!a.lens) return fail(c, GPT2_ERR_CONFIG, "paged_attention: seq_lens are required");
+  const int vn = kv->dtype == GPT2_BF16 ? 8 : 4, hd = kv->head_dim;
+  if (!paged_rows_ok(a.q, a.ldq, a.nh, hd, vn) || !paged_rows_ok(a.out, a.ldo, a.nh, hd, vn))
+    return fail(c, GPT2_ERR_CONFIG,
+                "paged_attention: q and out must start and step on 16 bytes, with row strides of at least a row");
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < paged_attention_ws_bytes(kv->n_seqs, a.nh, a.c.nkv, hd))
+    return fail(c, GPT2_ERR_CONFIG, "paged_attention: workspace missing, misaligned or too small");
+  const dim3 grid(a.nh, kv->n_seqs);
+#define PAT(T, HDV) paged_attn_kernel<T, HDV><<<grid, PAT_THREADS, 0, c.stream>>>(a)
+#define PAT_HD(T)                 \
+  switch (hd) {                   \
+    case 32: PAT(T, 32); break;   \
+    case 64: PAT(T, 64); break;   \
+    case 96: PAT(T, 96); break;   \
+    default: PAT(T, 128);         \
+  }
+  if (kv->dtype == GPT2_BF16) {
+    PAT_HD(bf16)
+  } else {
+    PAT_HD(float)
+  }
+#undef PAT_HD
+#undef PAT
+  return check_launch(c, "paged_attention");
 }
 
 }  // namespace g2
