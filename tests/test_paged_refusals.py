@@ -53,6 +53,7 @@ BAD_CACHES = [
     (dict(page_size=8192), CONFIG), (dict(table_stride=7), CONFIG), (dict(page_stride=2052), CONFIG),
     (dict(row_stride=-128), CONFIG), (dict(head_stride=4), CONFIG),
     (dict(max_pages=1 << 20, table_stride=1 << 20, page_size=2048), TOO_LONG),
+    (dict(max_pages=1 << 20, table_stride=1 << 20, page_size=512, n_seqs=33), TOO_LONG),
 ]
 
 
@@ -111,8 +112,9 @@ def test_workspace_size():
 
 
 INDEX_CHECK = r"""
-#include <cstdio>
+#include <cstdlib>
 #include <set>
+#include <vector>
 #include "paged_index.cuh"
 using namespace g2;
 int main() {
@@ -141,6 +143,41 @@ int main() {
   if (paged_length(11, 10, &bad) != 10 || !bad) return 6;
   bad = 0;
   if (paged_length(-3, 10, &bad) != 0 || !bad) return 7;
+
+  // every worker's walk over its share, one after the other, is the whole order
+  srand(1);
+  for (int trial = 0; trial < 3000; ++trial) {
+    const int n_seqs = 1 + rand() % 9, items = 1 + rand() % 5, workers = 1 + rand() % 40, least = 1 + rand() % 6;
+    std::vector<int> before(n_seqs + 1, 0);
+    for (int b = 0; b < n_seqs; ++b) before[b + 1] = before[b] + (rand() % 3 ? paged_tiles(rand() % 200) : 0);
+    const int64_t total = (int64_t)before[n_seqs] * items, share = paged_share(total, workers, least);
+    if (share < least || share * workers < total) return 8;
+    int64_t u = 0;
+    int seq = -1, item = items - 1, tile = 0, tiles = 1;  // the walk that is expected
+    for (int w = 0; w < workers; ++w) {
+      const int64_t a = w * share, e = a + share < total ? a + share : total;
+      if (a >= e) continue;
+      PagedCursor c = paged_locate(before.data(), n_seqs, items, a);
+      for (int64_t i = a; i < e; ++i, ++u) {
+        if (i > a) {
+          const int was = c.seq;
+          if (paged_next(c, before.data(), items) != (c.seq != was)) return 9;
+        }
+        if (u == 0 || ++tile >= tiles) {
+          tile = 0;
+          if (++item >= items) {
+            item = 0;
+            do ++seq;
+            while (before[seq + 1] == before[seq]);
+            tiles = before[seq + 1] - before[seq];
+          }
+        }
+        if (c.seq != seq || c.item != item || c.tile != tile || c.tiles != tiles) return 10;
+      }
+    }
+    if (u != total) return 11;
+  }
+  if (paged_tiles(0) != 0 || paged_tiles(1) != 1 || paged_tiles(16) != 1 || paged_tiles(17) != 2) return 12;
   return 0;
 }
 """

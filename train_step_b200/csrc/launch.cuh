@@ -1164,6 +1164,8 @@ inline int paged_view(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedView* ou
     return fail(c, GPT2_ERR_CONFIG, "paged cache: k, v and the strides must be multiples of 16 bytes");
   if ((reinterpret_cast<uintptr_t>(kv->page_table) | reinterpret_cast<uintptr_t>(kv->status)) & 3)
     return fail(c, GPT2_ERR_CONFIG, "paged cache: page_table and status must be 4-byte aligned");
+  if ((int64_t)kv->max_pages * kv->page_size * kv->n_seqs > (1LL << 34))
+    return fail(c, GPT2_ERR_SEQ_TOO_LONG, "paged cache: more than 2^34 tokens in all sequences");
   int lg = 0;
   while ((1 << lg) < kv->page_size) ++lg;
   *out = PagedView{kv->k,      kv->v,      kv->page_stride, kv->row_stride, kv->head_stride,
@@ -1214,9 +1216,54 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedApp
 
 inline bool paged_heads_ok(int nh, int nkv) { return nkv >= 1 && nh >= 1 && nh <= 4096 && nh % nkv == 0; }
 
+// Partial results of at most PAT_MAX_WORKERS workers: two each, of min(16, group) rows.
 inline size_t paged_attention_ws_bytes(int n_seqs, int nh, int nkv, int hd) {
-  if (n_seqs < 0 || n_seqs > PAGED_MAX_SEQS || !paged_heads_ok(nh, nkv) || hd < 1) return 0;
-  return 16;
+  if (n_seqs < 0 || n_seqs > PAGED_MAX_SEQS || !paged_heads_ok(nh, nkv) || hd < 1 || hd > 128) return 0;
+  const size_t rows = std::min(16, nh / nkv);
+  return (size_t)PAT_MAX_WORKERS * (8 + 2 * rows * (8 + (size_t)hd * 4));
+}
+
+template <class T, int HD, int QR>
+int paged_attention_inst(const LaunchCtx& c, const PagedAttnArgs& a, void* ws) {
+  using S = PatShape<T, HD, QR>;
+  const size_t smem = S::smem(a.c.n_seqs);
+  static_assert(S::smem(PAGED_MAX_SEQS) <= 226 * 1024, "ring too large");
+  if (!smem_optin(paged_attn_kernel<T, HD, QR>, (int)S::smem(PAGED_MAX_SEQS)))
+    return fail(c, GPT2_ERR_CUDA, "paged_attention: shared memory opt-in failed");
+  const int grid = std::min(c.num_sms, PAT_MAX_WORKERS / S::WARPS);
+  PagedAttnPlan pl;
+  pl.workers = grid * S::WARPS;
+  pl.group = a.nh / a.c.nkv;
+  pl.rows = std::min(QR, pl.group);
+  pl.qtiles = (pl.group + QR - 1) / QR;
+  pl.items = a.c.nkv * pl.qtiles;
+  char* p = static_cast<char*>(ws);
+  pl.part = reinterpret_cast<float*>(p);  // every part a multiple of 16 bytes
+  p += (size_t)pl.workers * 2 * pl.rows * HD * 4;
+  pl.ml = reinterpret_cast<float2*>(p);
+  p += (size_t)pl.workers * 2 * pl.rows * 8;
+  pl.rec = reinterpret_cast<int*>(p);
+  paged_attn_kernel<T, HD, QR><<<grid, S::WARPS * 32, smem, c.stream>>>(a, pl);
+  int r = check_launch(c, "paged_attention");
+  if (r) return r;
+  LaunchCtx cj = c;
+  cj.pdl = true;  // the join's blocks wait on the device for the kernel before
+  const cudaError_t e =
+      launch_k(cj, paged_join_kernel<T, HD>, dim3(pl.workers), dim3(PAJ_THREADS), 0, a, pl, (int)QR);
+  if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_join: ") + cudaGetErrorString(e));
+  return check_launch(c, "paged_join");
+}
+
+// The smallest query tile that holds the group: 8 or 16 rows of a tensor-core product in bf16,
+// 1, 4 or 8 rows of fp32 arithmetic. Larger groups take several tiles, which read the keys once
+// each.
+template <int HD>
+int paged_attention_hd(const LaunchCtx& c, bool bf, const PagedAttnArgs& a, void* ws) {
+  const int group = a.nh / a.c.nkv;
+  if (bf) return group <= 8 ? paged_attention_inst<bf16, HD, 8>(c, a, ws) : paged_attention_inst<bf16, HD, 16>(c, a, ws);
+  return group == 1   ? paged_attention_inst<float, HD, 1>(c, a, ws)
+         : group <= 4 ? paged_attention_inst<float, HD, 4>(c, a, ws)
+                      : paged_attention_inst<float, HD, 8>(c, a, ws);
 }
 
 inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedAttnArgs a, void* ws, size_t ws_bytes) {
@@ -1234,23 +1281,13 @@ inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedAtt
                 "paged_attention: q and out must start and step on 16 bytes, with row strides of at least a row");
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < paged_attention_ws_bytes(kv->n_seqs, a.nh, a.c.nkv, hd))
     return fail(c, GPT2_ERR_CONFIG, "paged_attention: workspace missing, misaligned or too small");
-  const dim3 grid(a.nh, kv->n_seqs);
-#define PAT(T, HDV) paged_attn_kernel<T, HDV><<<grid, PAT_THREADS, 0, c.stream>>>(a)
-#define PAT_HD(T)                 \
-  switch (hd) {                   \
-    case 32: PAT(T, 32); break;   \
-    case 64: PAT(T, 64); break;   \
-    case 96: PAT(T, 96); break;   \
-    default: PAT(T, 128);         \
+  const bool bf = kv->dtype == GPT2_BF16;
+  switch (hd) {
+    case 32: return paged_attention_hd<32>(c, bf, a, ws);
+    case 64: return paged_attention_hd<64>(c, bf, a, ws);
+    case 96: return paged_attention_hd<96>(c, bf, a, ws);
+    default: return paged_attention_hd<128>(c, bf, a, ws);
   }
-  if (kv->dtype == GPT2_BF16) {
-    PAT_HD(bf16)
-  } else {
-    PAT_HD(float)
-  }
-#undef PAT_HD
-#undef PAT
-  return check_launch(c, "paged_attention");
 }
 
 }  // namespace g2
