@@ -1249,7 +1249,8 @@ int paged_attention_inst(const LaunchCtx& c, const PagedAttnArgs& a, void* ws) {
   LaunchCtx cj = c;
   cj.pdl = true;  // the join's blocks wait on the device for the kernel before
   const cudaError_t e =
-      launch_k(cj, paged_join_kernel<T, HD>, dim3(pl.workers), dim3(PAJ_THREADS), 0, a, pl, (int)QR);
+      launch_k(cj, paged_join_kernel<T, HD>, dim3((pl.workers + PAJ_WORKERS - 1) / PAJ_WORKERS, pl.rows),
+               dim3(PAJ_THREADS), 0, a, pl, (int)QR);
   if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_join: ") + cudaGetErrorString(e));
   return check_launch(c, "paged_join");
 }

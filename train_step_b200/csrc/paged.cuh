@@ -721,69 +721,90 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::WARPS * 32, 1)
   }
 }
 
-// Joins the partial results of the item that begins in worker blockIdx.x and goes on in later
-// ones (none: nothing to do): o = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M), M = max m_i.
-// A thread holds four output elements of a row over every PARTS-th partial result.
-constexpr int PAJ_THREADS = 256;
+// Joins the partial results of the items that begin in workers 8 blockIdx.x ... + 7 and go on in
+// later ones: o = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M), M = max m_i. A block does the
+// rows blockIdx.y, + gridDim.y, ...; a thread holds four output elements over every PARTS-th
+// partial result, with the loads of PAJ_AHEAD of them in flight.
+constexpr int PAJ_THREADS = 256, PAJ_WORKERS = 8, PAJ_AHEAD = 4;
 template <class T, int HD>
 __global__ void __launch_bounds__(PAJ_THREADS) paged_join_kernel(const PagedAttnArgs a, const PagedAttnPlan pl, int qr) {
   constexpr int VEC = HD / 4, PARTS = PAJ_THREADS / VEC;
   __shared__ float4 s_o[PARTS][VEC];
   __shared__ float2 s_ml[PARTS];
+  __shared__ int2 s_rec[PAJ_WORKERS];
   pdl_wait();
-  const int w0 = blockIdx.x, w1 = pl.rec[2 * w0 + 1];
-  if (w1 < 0) return;
-  const int id = pl.rec[2 * w0], b = id / pl.items, item = id - b * pl.items;
-  const int hk = item / pl.qtiles, q0 = (item - hk * pl.qtiles) * qr, rows = min(qr, pl.group - q0);
+  const int base = blockIdx.x * PAJ_WORKERS;
+  if (threadIdx.x < PAJ_WORKERS)
+    s_rec[threadIdx.x] =
+        base + (int)threadIdx.x < pl.workers ? *reinterpret_cast<const int2*>(pl.rec + 2 * (base + threadIdx.x)) : make_int2(0, -1);
+  __syncthreads();
   const int v = threadIdx.x % VEC, p = threadIdx.x / VEC;
-  for (int r = 0; r < rows; ++r) {
-    if (p < PARTS) {
-      float m = -INFINITY, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = w0 + p; w <= w1; w += PARTS) {
-        const int64_t i = ((int64_t)w * 2 + (w == w1 ? 0 : 1)) * pl.rows + r;
-        const float2 ml = pl.ml[i];
-        const float4 x = *reinterpret_cast<const float4*>(pl.part + i * HD + v * 4);
-        const float mn = fmaxf(m, ml.x);
-        if (mn == -INFINITY) continue;
-        const float f = exp2f(m - mn), g = exp2f(ml.x - mn);
-        m = mn;
-        l = l * f + ml.y * g;
-        o.x = o.x * f + x.x * g;
-        o.y = o.y * f + x.y * g;
-        o.z = o.z * f + x.z * g;
-        o.w = o.w * f + x.w * g;
+  for (int k = 0; k < PAJ_WORKERS; ++k) {
+    const int w0 = base + k, w1 = s_rec[k].y;
+    if (w1 < 0) continue;
+    const int id = s_rec[k].x, b = id / pl.items, item = id - b * pl.items;
+    const int hk = item / pl.qtiles, q0 = (item - hk * pl.qtiles) * qr, rows = min(qr, pl.group - q0);
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+      if (p < PARTS) {
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = w0 + p; w <= w1; w += PARTS * PAJ_AHEAD) {
+          float2 ml[PAJ_AHEAD];
+          float4 x[PAJ_AHEAD];
+#pragma unroll
+          for (int j = 0; j < PAJ_AHEAD; ++j) {
+            const int wj = w + j * PARTS;
+            const int64_t i = ((int64_t)wj * 2 + (wj == w1 ? 0 : 1)) * pl.rows + r;
+            ml[j] = make_float2(-INFINITY, 0.f);
+            if (wj <= w1) {
+              ml[j] = pl.ml[i];
+              x[j] = *reinterpret_cast<const float4*>(pl.part + i * HD + v * 4);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < PAJ_AHEAD; ++j) {
+            const float mn = fmaxf(m, ml[j].x);
+            if (ml[j].x == -INFINITY) continue;  // past the end, or nothing visible in the piece
+            const float f = exp2f(m - mn), g = exp2f(ml[j].x - mn);
+            m = mn;
+            l = l * f + ml[j].y * g;
+            o.x = o.x * f + x[j].x * g;
+            o.y = o.y * f + x[j].y * g;
+            o.z = o.z * f + x[j].z * g;
+            o.w = o.w * f + x[j].w * g;
+          }
+        }
+        s_o[p][v] = o;
+        if (v == 0) s_ml[p] = make_float2(m, l);
       }
-      s_o[p][v] = o;
-      if (v == 0) s_ml[p] = make_float2(m, l);
-    }
-    __syncthreads();
-    if (p == 0) {
-      float M = -INFINITY;
-      for (int i = 0; i < PARTS; ++i) M = fmaxf(M, s_ml[i].x);
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < PARTS; ++i) {
-        const float2 ml = s_ml[i];
-        if (ml.x == -INFINITY) continue;
-        const float g = exp2f(ml.x - M);
-        const float4 x = s_o[i][v];
-        l += ml.y * g;
-        o.x += x.x * g;
-        o.y += x.y * g;
-        o.z += x.z * g;
-        o.w += x.w * g;
+      __syncthreads();
+      if (p == 0) {
+        float M = -INFINITY;
+        for (int i = 0; i < PARTS; ++i) M = fmaxf(M, s_ml[i].x);
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < PARTS; ++i) {
+          const float2 ml = s_ml[i];
+          if (ml.x == -INFINITY) continue;
+          const float g = exp2f(ml.x - M);
+          const float4 x = s_o[i][v];
+          l += ml.y * g;
+          o.x += x.x * g;
+          o.y += x.y * g;
+          o.z += x.z * g;
+          o.w += x.w * g;
+        }
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        const int h = hk * pl.group + q0 + r;
+        T* out = static_cast<T*>(a.out) + b * a.ldo + h * HD + v * 4;
+        out[0] = from_f32<T>(o.x * f);
+        out[1] = from_f32<T>(o.y * f);
+        out[2] = from_f32<T>(o.z * f);
+        out[3] = from_f32<T>(o.w * f);
+        if (a.lse && v == 0) a.lse[(int64_t)b * a.nh + h] = l == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(l);
       }
-      const float f = l == 0.f ? 0.f : 1.f / l;
-      const int h = hk * pl.group + q0 + r;
-      T* out = static_cast<T*>(a.out) + b * a.ldo + h * HD + v * 4;
-      out[0] = from_f32<T>(o.x * f);
-      out[1] = from_f32<T>(o.y * f);
-      out[2] = from_f32<T>(o.z * f);
-      out[3] = from_f32<T>(o.w * f);
-      if (a.lse && v == 0) a.lse[(int64_t)b * a.nh + h] = l == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(l);
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
