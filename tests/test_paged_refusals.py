@@ -118,26 +118,30 @@ INDEX_CHECK = r"""
 #include "paged_index.cuh"
 using namespace g2;
 int main() {
-  for (int len = 0; len < 40; ++len)
-    for (int window = 0; window < 45; ++window)
-      for (int sinks = 0; sinks < 45; ++sinks) {
+  for (int len = 0; len < 70; ++len)
+    for (int window = 0; window < 75; ++window)
+      for (int sinks = 0; sinks < 75; ++sinks) {
         std::set<int> want, got;
         for (int j = 0; j < len; ++j)
           if (window == 0 || j >= len - window || j < sinks) want.insert(j);
         const PagedVisible v = paged_visible(len, window, sinks);
         int last = -1;
-        for (int i = 0; i < v.count; ++i) {
-          const int p = paged_position(v, i);
-          if (p <= last) return 1;
-          last = p;
-          got.insert(p);
+        for (int t = 0; t < v.tiles; ++t) {
+          const int pos = paged_tile_pos(v, t);
+          const uint32_t mask = paged_tile_mask(v, pos);
+          if (pos % PAT_TILE || pos <= last || mask == 0 || mask > 0xffff) return 1;
+          last = pos;
+          for (int i = 0; i < PAT_TILE; ++i)
+            if (mask >> i & 1) got.insert(pos + i);
         }
         if (got != want) return 2;
       }
   // the extremes do not overflow
   const int big = 1 << 30, most = 0x7fffffff;
-  if (paged_visible(big, most, most).count != big || paged_visible(big, 1, most).count != big) return 3;
-  if (paged_visible(big, 1, 0).count != 1 || paged_position(paged_visible(big, 1, 0), 0) != big - 1) return 4;
+  if (paged_visible(big, most, most).tiles != big / 16 || paged_visible(big, 1, most).tiles != big / 16) return 3;
+  const PagedVisible one = paged_visible(big, 1, 0);
+  if (one.tiles != 1 || paged_tile_pos(one, 0) != big - 16 || paged_tile_mask(one, big - 16) != 0x8000) return 4;
+  if (paged_div(7, 2) != 3 || paged_div(1LL << 40, 3) != (1LL << 40) / 3 || paged_div(0xffffffffLL, 1) != 0xffffffffLL) return 13;
   int bad = 0;
   if (paged_length(5, 10, &bad) != 5 || paged_length(10, 10, &bad) != 10 || bad) return 5;
   if (paged_length(11, 10, &bad) != 10 || !bad) return 6;
@@ -147,11 +151,11 @@ int main() {
   // every worker's walk over its share, one after the other, is the whole order
   srand(1);
   for (int trial = 0; trial < 3000; ++trial) {
-    const int n_seqs = 1 + rand() % 9, items = 1 + rand() % 5, workers = 1 + rand() % 40, least = 1 + rand() % 6;
+    const int n_seqs = 1 + rand() % 9, items = 1 + rand() % 5, workers = 1 + rand() % 40;
     std::vector<int> before(n_seqs + 1, 0);
-    for (int b = 0; b < n_seqs; ++b) before[b + 1] = before[b] + (rand() % 3 ? paged_tiles(rand() % 200) : 0);
-    const int64_t total = (int64_t)before[n_seqs] * items, share = paged_share(total, workers, least);
-    if (share < least || share * workers < total) return 8;
+    for (int b = 0; b < n_seqs; ++b) before[b + 1] = before[b] + (rand() % 3 ? rand() % 14 : 0);
+    const int64_t total = (int64_t)before[n_seqs] * items, share = paged_share(total, workers);
+    if (share < 1 || share * workers < total) return 8;
     int64_t u = 0;
     int seq = -1, item = items - 1, tile = 0, tiles = 1;  // the walk that is expected
     for (int w = 0; w < workers; ++w) {
@@ -177,7 +181,6 @@ int main() {
     }
     if (u != total) return 11;
   }
-  if (paged_tiles(0) != 0 || paged_tiles(1) != 1 || paged_tiles(16) != 1 || paged_tiles(17) != 2) return 12;
   return 0;
 }
 """

@@ -634,6 +634,11 @@ class PagedKV:
                            hs if self.n_kv_heads > 1 else 0, _ptr(page_table), ts, _ptr(self.status), _dt(k_cache),
                            n_pages, page_size, max_pages, self.n_seqs, self.n_kv_heads, self.head_dim)
         self._ref = ct.byref(self._c)
+        # looked up once: a call takes a few microseconds
+        self._append, self._attention = lib().gpt2_op_paged_kv_append, lib().gpt2_op_paged_attention
+        self._index, self._scale = k_cache.get_device(), self.head_dim ** -0.5
+        self._int32, self._float32 = torch.int32, torch.float32
+        self._current_device, self._current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
     def attention_workspace(self, n_heads: int):
         """A workspace for paged_attention with n_heads query heads (one per concurrent call)."""
@@ -644,41 +649,34 @@ class PagedKV:
     def check(self, stream=None) -> None:
         """Wait for the stream and raise Gpt2Error(GPT2_ERR_PAGE_RANGE) if a call on this cache
         met a bad page id, sequence, position or length since the last check."""
-        with _device_of(self.device):
-            _op(lib().gpt2_op_paged_status(self._ref, _stream(stream)))
+        self._call(lib().gpt2_op_paged_status, (), stream)
 
-    def _rows(self, name, t, n_heads=None):
-        """[N, heads, head_dim] rows of the cache's type and device: their row stride."""
-        if (t.dim() != 3 or t.dtype != self.dtype or t.device != self.device or t.shape[2] != self.head_dim
-                or (n_heads is not None and t.shape[1] != n_heads)):
-            raise ValueError(f"{name} must be [N, {n_heads or 'heads'}, {self.head_dim}] {self.dtype} on {self.device}")
-        N, H, D = t.shape
+    def _rows(self, name, t, rows, heads):
+        """[rows, heads, head_dim] of the cache's type and device, heads contiguous: the row stride."""
         st = t.stride()
-        if st[2] != 1 or (H > 1 and st[1] != D):
-            raise ValueError(f"{name}: the heads of a row must be contiguous")
-        return st[0] if N > 1 else H * D
+        if (tuple(t.shape) != (rows, heads, self.head_dim) or t.dtype is not self.dtype
+                or t.get_device() != self._index or st[2] != 1 or (st[1] != self.head_dim and heads > 1)):
+            raise ValueError(f"{name} must be [{rows}, {heads}, {self.head_dim}] {self.dtype} on {self.device}, "
+                             "with the heads of a row contiguous")
+        return st[0] if rows > 1 else heads * self.head_dim
 
     def _ints(self, name, t, n):
-        import torch
-        if t.dtype != torch.int32 or t.shape != (n,) or t.device != self.device or (n > 1 and t.stride(0) != 1):
+        if (t.dtype is not self._int32 or tuple(t.shape) != (n,) or t.get_device() != self._index
+                or (t.stride(0) != 1 and n > 1)):
             raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {self.device}")
+        return t.data_ptr()
 
-
-class _NoContext:
-    def __enter__(self):
-        pass
-
-    def __exit__(self, *a):
-        pass
-
-
-_NO_CONTEXT = _NoContext()
-
-
-def _device_of(device):
-    """Makes `device` current for a call when it is not."""
-    import torch
-    return _NO_CONTEXT if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    def _call(self, f, args, stream) -> None:
+        """f(cache, *args, stream) with the cache's device current; torch's current stream of that
+        device by default."""
+        if self._current_device() == self._index:
+            rc = f(self._ref, *args, self._current_stream(self._index) if stream is None else stream)
+        else:
+            import torch
+            with torch.cuda.device(self._index):
+                rc = f(self._ref, *args, self._current_stream(self._index) if stream is None else stream)
+        if rc:
+            _op(rc)
 
 
 def paged_kv_append(cache: PagedKV, k, v, positions, seqs=None, q=None, q_out=None, cos_sin=None,
@@ -687,31 +685,26 @@ def paged_kv_append(cache: PagedKV, k, v, positions, seqs=None, q=None, q_out=No
     positions[n] (int32; negative: a padding row) of sequence seqs[n] (int32; None: n). With
     cos_sin (fp32 [n_positions, rot_dim], see rotation_table) keys are rotated on the way, and
     q [N, n_heads, head_dim] is rotated into q_out (may be q). See gpt2_op_paged_kv_append."""
-    import torch
     N = k.shape[0]
-    ldk, ldv = cache._rows("k", k, cache.n_kv_heads), cache._rows("v", v, cache.n_kv_heads)
-    cache._ints("positions", positions, N)
-    if seqs is not None:
-        cache._ints("seqs", seqs, N)
-    nh = ldq = ldqo = 0
-    if (q is None) != (q_out is None):
+    ldk, ldv = cache._rows("k", k, N, cache.n_kv_heads), cache._rows("v", v, N, cache.n_kv_heads)
+    pos = cache._ints("positions", positions, N)
+    seq = None if seqs is None else cache._ints("seqs", seqs, N)
+    nh = ldq = ldqo = n_pos = rot = 0
+    pq = pqo = pcs = None
+    if q is not None and q_out is not None:
+        nh = q.shape[1] if q.dim() == 3 else 1
+        ldq, ldqo = cache._rows("q", q, N, nh), cache._rows("q_out", q_out, N, nh)
+        pq, pqo = q.data_ptr(), q_out.data_ptr()
+    elif q is not q_out:
         raise ValueError("q and q_out go together")
-    if q is not None:
-        nh = q.shape[1] if q.dim() == 3 else 0
-        ldq, ldqo = cache._rows("q", q, nh), cache._rows("q_out", q_out, nh)
-        if q.shape[0] != N or q_out.shape[0] != N:
-            raise ValueError("q and q_out must have a row per token")
-    if v.shape[0] != N:
-        raise ValueError("k and v must have a row per token")
-    n_pos = rot = 0
     if cos_sin is not None:
-        if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != cache.device                 or not cos_sin.is_contiguous():
+        if (cos_sin.dim() != 2 or cos_sin.dtype is not cache._float32 or cos_sin.get_device() != cache._index
+                or not cos_sin.is_contiguous()):
             raise ValueError(f"cos_sin must be a contiguous fp32 tensor [n_positions, rot_dim] on {cache.device}")
         n_pos, rot = cos_sin.shape
-    with _device_of(cache.device):
-        _op(lib().gpt2_op_paged_kv_append(cache._ref, _ptr(k), ldk, _ptr(v), ldv, _ptr(q), ldq, _ptr(q_out), ldqo, nh,
-                                          N, _ptr(positions), _ptr(seqs), _ptr(cos_sin), n_pos, rot,
-                                          int(interleaved), _stream(stream)))
+        pcs = cos_sin.data_ptr()
+    cache._call(cache._append, (k.data_ptr(), ldk, v.data_ptr(), ldv, pq, ldq, pqo, ldqo, nh, N, pos, seq, pcs, n_pos,
+                                rot, int(interleaved)), stream)
 
 
 def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None, window: int = 0, sinks: int = 0,
@@ -721,25 +714,24 @@ def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None
     newest `window` and the first `sinks`. lse: optional fp32 [n_seqs, n_heads]. scale: 1 /
     sqrt(head_dim) by default. ws: cache.attention_workspace(n_heads), to be kept between calls
     (None: allocated for this one). See gpt2_op_paged_attention."""
-    import torch
-    nh = q.shape[1] if q.dim() == 3 else 0
-    ldq, ldo = cache._rows("q", q, nh), cache._rows("out", out, nh)
-    if q.shape[0] != cache.n_seqs or out.shape[0] != cache.n_seqs:
-        raise ValueError(f"q and out must have a row per sequence ({cache.n_seqs})")
-    cache._ints("seq_lens", seq_lens, cache.n_seqs)
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (cache.n_seqs, nh) or not lse.is_contiguous()
-                            or lse.device != cache.device):
-        raise ValueError(f"lse must be a contiguous fp32 tensor [{cache.n_seqs}, {nh}] on {cache.device}")
-    with _device_of(cache.device):
-        if ws is None:
-            if stream is not None:
-                raise ValueError("a call on an explicit stream needs its own workspace")
-            ws = cache.attention_workspace(nh)
-        elif ws.device != cache.device:
-            raise ValueError(f"ws must be on {cache.device}")
-        _op(lib().gpt2_op_paged_attention(cache._ref, _ptr(q), ldq, nh, _ptr(seq_lens),
-                                          cache.head_dim ** -0.5 if scale is None else scale, window, sinks, _ptr(out),
-                                          ldo, _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    B = cache.n_seqs
+    nh = q.shape[1] if q.dim() == 3 else 1
+    ldq, ldo = cache._rows("q", q, B, nh), cache._rows("out", out, B, nh)
+    lens = cache._ints("seq_lens", seq_lens, B)
+    pl = None
+    if lse is not None:
+        if (lse.dtype is not cache._float32 or tuple(lse.shape) != (B, nh) or lse.get_device() != cache._index
+                or not lse.is_contiguous()):
+            raise ValueError(f"lse must be a contiguous fp32 tensor [{B}, {nh}] on {cache.device}")
+        pl = lse.data_ptr()
+    if ws is None:
+        if stream is not None:
+            raise ValueError("a call on an explicit stream needs its own workspace")
+        ws = cache.attention_workspace(nh)
+    elif ws.get_device() != cache._index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {cache.device}")
+    cache._call(cache._attention, (q.data_ptr(), ldq, nh, lens, cache._scale if scale is None else scale, window, sinks,
+                                   out.data_ptr(), ldo, pl, ws.data_ptr(), ws.nbytes), stream)
 
 
 def rotation_table(n_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):

@@ -5,6 +5,8 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <cstdio>
 #include <map>
 #include <mutex>
@@ -1216,55 +1218,95 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedApp
 
 inline bool paged_heads_ok(int nh, int nkv) { return nkv >= 1 && nh >= 1 && nh <= 4096 && nh % nkv == 0; }
 
-// Partial results of at most PAT_MAX_WORKERS workers: two each, of min(16, group) rows.
+// Partial results of at most PAT_MAX_BLOCKS blocks: two each, of min(16, group) rows; and an
+// arrival word each.
 inline size_t paged_attention_ws_bytes(int n_seqs, int nh, int nkv, int hd) {
   if (n_seqs < 0 || n_seqs > PAGED_MAX_SEQS || !paged_heads_ok(nh, nkv) || hd < 1 || hd > 128) return 0;
   const size_t rows = std::min(16, nh / nkv);
-  return (size_t)PAT_MAX_WORKERS * (8 + 2 * rows * (8 + (size_t)hd * 4));
+  return (size_t)PAT_MAX_BLOCKS * (8 + 2 * rows * (8 + (size_t)hd * 4));
 }
 
-template <class T, int HD, int QR>
-int paged_attention_inst(const LaunchCtx& c, const PagedAttnArgs& a, void* ws) {
+// A number that no other call of this process has, and that what a workspace happens to hold
+// does not have either (48 random bits of it would have to agree).
+inline unsigned long long paged_call_tag() {
+  static std::atomic<unsigned long long> next{
+      (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() ^
+      ((unsigned long long)reinterpret_cast<uintptr_t>(&paged_call_tag) << 20)};
+  unsigned long long z = next.fetch_add(0x9E3779B97F4A7C15ull);
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  z ^= z >> 31;
+  return (z | (1ull << 63)) & ~((1ull << PAT_COUNT_BITS) - 1);
+}
+
+// A pool as a 4-D tensor {head_dim, page_size, n_kv_heads, n_pages}; box: 16 tokens of one head
+// and page, up to 128 bytes wide. A stride of a dimension of one element is not used; false for
+// strides that a tensor map does not take (0, as of an expanded tensor, or 2^40 bytes and more).
+inline bool encode_paged_map(CUtensorMap* map, const void* ptr, const gpt2_paged_kv* kv) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const bool bf = kv->dtype == GPT2_BF16;
+  const int64_t es = bf ? 2 : 4;
+  auto stride = [&](int64_t s, int n) { return (cuuint64_t)(n == 1 ? kv->head_dim * es : s * es); };
+  cuuint64_t dims[4] = {(cuuint64_t)kv->head_dim, (cuuint64_t)kv->page_size, (cuuint64_t)kv->n_kv_heads,
+                        (cuuint64_t)kv->n_pages};
+  cuuint64_t strides[3] = {stride(kv->row_stride, kv->page_size), stride(kv->head_stride, kv->n_kv_heads),
+                           stride(kv->page_stride, kv->n_pages)};
+  for (cuuint64_t s : strides)
+    if (s == 0) return false;
+  const int row = (int)std::min<int64_t>(128, kv->head_dim * es);
+  cuuint32_t box[4] = {(cuuint32_t)(row / es), (cuuint32_t)PAT_TILE, 1u, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(map, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(ptr),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             row == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, int HD, int QR, bool BOX>
+int paged_attention_inst(const LaunchCtx& c, const gpt2_paged_kv* kv, const PagedAttnArgs& a, void* ws) {
   using S = PatShape<T, HD, QR>;
-  const size_t smem = S::smem(a.c.n_seqs);
-  static_assert(S::smem(PAGED_MAX_SEQS) <= 226 * 1024, "ring too large");
-  if (!smem_optin(paged_attn_kernel<T, HD, QR>, (int)S::smem(PAGED_MAX_SEQS)))
+  constexpr int SMEM_MAX = 226 * 1024;
+  static_assert(S::warps(QR) >= 1 && S::smem(QR, PAGED_MAX_SEQS) <= SMEM_MAX && S::smem(1, PAGED_MAX_SEQS) <= SMEM_MAX,
+                "rings too large");
+  CUtensorMap km{}, vm{};
+  if (BOX && (!encode_paged_map(&km, kv->k, kv) || !encode_paged_map(&vm, kv->v, kv)))
+    return paged_attention_inst<T, HD, QR, false>(c, kv, a, ws);
+  if (!smem_optin(paged_attn_kernel<T, HD, QR, BOX>, SMEM_MAX))
     return fail(c, GPT2_ERR_CUDA, "paged_attention: shared memory opt-in failed");
-  const int grid = std::min(c.num_sms, PAT_MAX_WORKERS / S::WARPS);
   PagedAttnPlan pl;
-  pl.workers = grid * S::WARPS;
   pl.group = a.nh / a.c.nkv;
   pl.rows = std::min(QR, pl.group);
+  pl.warps = S::warps(pl.rows);
+  const int grid = std::min(c.num_sms, PAT_MAX_BLOCKS);
+  pl.workers = grid * pl.warps;
   pl.qtiles = (pl.group + QR - 1) / QR;
   pl.items = a.c.nkv * pl.qtiles;
+  pl.tag = paged_call_tag();
   char* p = static_cast<char*>(ws);
   pl.part = reinterpret_cast<float*>(p);  // every part a multiple of 16 bytes
-  p += (size_t)pl.workers * 2 * pl.rows * HD * 4;
+  p += (size_t)grid * 2 * pl.rows * HD * 4;
   pl.ml = reinterpret_cast<float2*>(p);
-  p += (size_t)pl.workers * 2 * pl.rows * 8;
-  pl.rec = reinterpret_cast<int*>(p);
-  paged_attn_kernel<T, HD, QR><<<grid, S::WARPS * 32, smem, c.stream>>>(a, pl);
-  int r = check_launch(c, "paged_attention");
-  if (r) return r;
-  LaunchCtx cj = c;
-  cj.pdl = true;  // the join's blocks wait on the device for the kernel before
-  const cudaError_t e =
-      launch_k(cj, paged_join_kernel<T, HD>, dim3((pl.workers + PAJ_WORKERS - 1) / PAJ_WORKERS, pl.rows),
-               dim3(PAJ_THREADS), 0, a, pl, (int)QR);
-  if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_join: ") + cudaGetErrorString(e));
-  return check_launch(c, "paged_join");
+  p += (size_t)grid * 2 * pl.rows * 8;
+  pl.arrived = reinterpret_cast<unsigned long long*>(p);
+  const cudaError_t e = launch_k(c, paged_attn_kernel<T, HD, QR, BOX>, dim3(grid), dim3(pl.warps * 32),
+                                 S::smem(pl.rows, a.c.n_seqs), a, pl, km, vm);
+  if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_attention: ") + cudaGetErrorString(e));
+  return check_launch(c, "paged_attention");
 }
 
 // The smallest query tile that holds the group: 8 or 16 rows of a tensor-core product in bf16,
 // 1, 4 or 8 rows of fp32 arithmetic. Larger groups take several tiles, which read the keys once
 // each.
-template <int HD>
-int paged_attention_hd(const LaunchCtx& c, bool bf, const PagedAttnArgs& a, void* ws) {
+template <int HD, bool BOX>
+int paged_attention_hd(const LaunchCtx& c, const gpt2_paged_kv* kv, const PagedAttnArgs& a, void* ws) {
   const int group = a.nh / a.c.nkv;
-  if (bf) return group <= 8 ? paged_attention_inst<bf16, HD, 8>(c, a, ws) : paged_attention_inst<bf16, HD, 16>(c, a, ws);
-  return group == 1   ? paged_attention_inst<float, HD, 1>(c, a, ws)
-         : group <= 4 ? paged_attention_inst<float, HD, 4>(c, a, ws)
-                      : paged_attention_inst<float, HD, 8>(c, a, ws);
+  if (kv->dtype == GPT2_BF16)
+    return group <= 8 ? paged_attention_inst<bf16, HD, 8, BOX>(c, kv, a, ws)
+                      : paged_attention_inst<bf16, HD, 16, BOX>(c, kv, a, ws);
+  return group == 1   ? paged_attention_inst<float, HD, 1, BOX>(c, kv, a, ws)
+         : group <= 4 ? paged_attention_inst<float, HD, 4, BOX>(c, kv, a, ws)
+                      : paged_attention_inst<float, HD, 8, BOX>(c, kv, a, ws);
 }
 
 inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedAttnArgs a, void* ws, size_t ws_bytes) {
@@ -1282,13 +1324,16 @@ inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedAtt
                 "paged_attention: q and out must start and step on 16 bytes, with row strides of at least a row");
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || ws_bytes < paged_attention_ws_bytes(kv->n_seqs, a.nh, a.c.nkv, hd))
     return fail(c, GPT2_ERR_CONFIG, "paged_attention: workspace missing, misaligned or too small");
-  const bool bf = kv->dtype == GPT2_BF16;
+  const bool box = kv->page_size >= PAT_TILE;
+#define PAT_HD(HD) \
+  return box ? paged_attention_hd<HD, true>(c, kv, a, ws) : paged_attention_hd<HD, false>(c, kv, a, ws)
   switch (hd) {
-    case 32: return paged_attention_hd<32>(c, bf, a, ws);
-    case 64: return paged_attention_hd<64>(c, bf, a, ws);
-    case 96: return paged_attention_hd<96>(c, bf, a, ws);
-    default: return paged_attention_hd<128>(c, bf, a, ws);
+    case 32: PAT_HD(32);
+    case 64: PAT_HD(64);
+    case 96: PAT_HD(96);
+    default: PAT_HD(128);
   }
+#undef PAT_HD
 }
 
 }  // namespace g2

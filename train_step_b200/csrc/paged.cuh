@@ -191,46 +191,93 @@ struct PagedAttnArgs {
 
 // Work split. A call has one item per (sequence, key head, tile of up to QR query heads of
 // that key head's group); an item is a run of 16-key tiles over its visible keys. The tiles of
-// all items are laid end to end and every warp of the grid (a worker) takes an equal share of
-// them, so ragged lengths balance without the host knowing them. A worker that takes an item
-// whole writes its output; pieces of an item go to the workspace and are joined by
-// paged_join_kernel. Each worker has at most one piece that begins inside an item and reaches
-// its end (slot 0) and one that does not reach the end (slot 1).
-// A worker streams its tiles through a ring of its own in shared memory with 16-byte
-// asynchronous copies, STAGES - 1 tiles ahead and on into the next item (the queries of an
-// item arrive with its first tile); it needs no barrier but the warp's.
-constexpr int PAT_MAX_WORKERS = 2048;
-constexpr int PAT_LEAST = 4;  // tiles of a share
-constexpr int PAT_SMEM = 184 * 1024;  // of the rings of a block
+// all items are laid end to end and every warp of the grid (a worker) takes an equal,
+// contiguous share of them, so ragged lengths balance without the host knowing them. A worker
+// that takes an item whole writes its output. Otherwise it leaves pieces in shared memory: at
+// most one that begins inside an item (its head piece) and one that begins with an item and does
+// not reach its end (its tail piece). When a block's workers are done, a warp joins the pieces
+// of each split item: to its output, or, for an item spread over several blocks, to a partial
+// result in the workspace (at most two per block: of the item that comes in from the block
+// before, slot 0, and of the one that goes on in the next, slot 1). The block that arrives last
+// at such an item joins its partial results, in their order, so results do not depend on the
+// order of arrival.
+// A worker streams its tiles through a ring of its own in shared memory, STAGES tiles ahead and
+// on into the next item (the queries of an item arrive with its first tile); it needs no barrier
+// but its own mbarriers and the warp's. With pages of 16 tokens or more (BOX) a tile is one
+// rectangle of a page and arrives by tensor copies that one lane issues; smaller pages, and
+// strides that a tensor map does not take, go through 16-byte copies by all lanes.
+// What bounds it: reading the cache from HBM, and, before that, the instructions of a warp (few
+// warps per scheduler, each a chain of dependent steps): 16-byte copies by all lanes took half
+// of a tile's instructions, which is what the tensor copies save.
+constexpr int PAT_MAX_BLOCKS = 256;
+constexpr int PAT_SMEM = 204 * 1024;  // of the workers of a block
 
 template <class T, int HD, int QR_>
 struct PatShape {
-  static constexpr int QR = QR_;               // query rows of an item
-  static constexpr int ROW = HD * sizeof(T);   // bytes
-  static constexpr int CPR = ROW / 16;         // 16-byte chunks per row
-  static constexpr int QOFF = 2 * PAT_TILE * ROW;
-  static constexpr int STAGE = QOFF + QR * ROW;  // keys, values, queries
-  static constexpr int STAGES = STAGE > 16384 ? 2 : STAGE > 12288 ? 3 : 4;
-  static constexpr int FIT = PAT_SMEM / (STAGES * STAGE);
-  static constexpr int WARPS = FIT > 12 ? 12 : FIT;
+  static constexpr int QR = QR_;              // query rows of an item, at most
+  static constexpr int ROW = HD * sizeof(T);  // bytes
+  static constexpr int CPR = ROW / 16;        // 16-byte chunks per row
+  // keys (and values) of a tile: boxes of 16 rows of up to 128 bytes
+  static constexpr int BOX_ROW = ROW < 128 ? ROW : 128;
+  static constexpr int BOXES = (ROW + BOX_ROW - 1) / BOX_ROW;
+  static constexpr int BOX = PAT_TILE * BOX_ROW;
+  static constexpr int TILE = BOXES * BOX;
+  static constexpr int STAGES = 2;
+  static constexpr int MAX_WARPS = 12;
   // fp32: a copy of the item's queries and the tile's weights, per warp
   static constexpr int SIDE = sizeof(T) == 4 ? QR * ROW + QR * PAT_TILE * 4 : 0;
-  // per warp: ring, side buffers, the validity masks of the stages
-  static constexpr int WARP_BYTES = STAGES * STAGE + SIDE + 16 * ((STAGES + 3) / 4);
-  static constexpr size_t smem(int n_seqs) { return (size_t)WARPS * WARP_BYTES + ((size_t)n_seqs + 1) * 4; }
+  // a piece: outputs, then (maximum, sum), of each row; a warp: its ring of keys and values
+  // (after the last tile: the tail piece), of queries, the head piece, the side buffers, the
+  // mbarriers and the validity masks of the stages
+  __host__ __device__ static constexpr int piece(int rows) { return rows * HD * 4 + (rows * 8 + 15) / 16 * 16; }
+  static constexpr int RING = STAGES * 2 * TILE;
+  __host__ __device__ static constexpr int head(int rows) { return RING + STAGES * rows * ROW; }
+  __host__ __device__ static constexpr int warp_bytes(int rows) {
+    return (head(rows) + piece(rows) + SIDE + STAGES * 12 + 1023) / 1024 * 1024;
+  }
+  static constexpr int warps(int rows) {
+    return PAT_SMEM / warp_bytes(rows) > MAX_WARPS ? MAX_WARPS : PAT_SMEM / warp_bytes(rows);
+  }
+  // the first 1024 bytes align the rest
+  static constexpr int smem(int rows, int n_seqs) { return 1024 + warps(rows) * warp_bytes(rows) + (n_seqs + 1) * 4; }
+
+  // 16-byte chunk `c` of row `r` in a tile: the order in which a tensor copy with 128-byte (64-byte
+  // for 64-byte rows) swizzling leaves it; consecutive rows of a chunk are in different banks
+  __device__ static __forceinline__ int chunk(int r, int c) {
+    if (BOX_ROW == 128) return (c >> 3) * BOX + r * 128 + (((c ^ r) & 7) << 4);
+    return r * BOX_ROW + ((c ^ ((r >> 1) & 3)) << 4);
+  }
 };
 
 struct PagedAttnPlan {
+  int warps;    // of a block
   int workers, items, qtiles, group, rows;  // rows: min(QR, group), the rows of a partial result
-  int* rec;                                 // [workers][2]: split item that begins in a worker, its last worker
-  float2* ml;                               // [workers][2][rows]: maximum (log2 units) and sum
-  float* part;                              // [workers][2][rows][HD]
+  unsigned long long tag;                   // of this call, in the bits above PAT_COUNT_BITS
+  unsigned long long* arrived;              // [blocks]: see pat_arrive
+  float2* ml;                               // [blocks][2][rows]: maximum (log2 units) and sum
+  float* part;                              // [blocks][2][rows][HD]
 };
 
-// chunk `c` of row `r` in a tile: consecutive rows at one chunk fall into different banks
-template <int CPR>
-__device__ __forceinline__ int pat_chunk(int r, int c) {
-  return r * CPR + (CPR % 8 == 0 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
+// Counts the blocks that have finished their part of one item in the word of its first block;
+// true for the n-th. A word belongs to this call only while it carries the call's tag, so it may
+// hold anything before the first arrival; the last one clears it, so that a captured call may run
+// again with the same tag.
+constexpr int PAT_COUNT_BITS = 16;
+__device__ __forceinline__ bool pat_arrive(unsigned long long* word, unsigned long long tag, int n) {
+  unsigned long long old = 0;  // what the last call that used the word has left
+  for (;;) {
+    const bool mine = (old >> PAT_COUNT_BITS) == (tag >> PAT_COUNT_BITS);
+    const int count = (mine ? (int)(old & ((1 << PAT_COUNT_BITS) - 1)) : 0) + 1;
+    const unsigned long long next = count == n ? 0ull : tag | (unsigned)count;
+    unsigned long long seen;
+    // releases this block's partial result, acquires those of the blocks that arrived before
+    asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
+                 : "=l"(seen)
+                 : "l"(word), "l"(old), "l"(next)
+                 : "memory");
+    if (seen == old) return count == n;
+    old = seen;  // another block arrived in between: at most n - 1 times
+  }
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
@@ -255,16 +302,15 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
 }
 
 // before[b] = tiles per item of sequences 0..b-1, for b <= n_seqs (whole block).
-template <int THREADS>
 __device__ __forceinline__ void pat_prefix(const PagedAttnArgs& a, int* before) {
-  __shared__ int wsum[THREADS / 32];
-  const int B = a.c.n_seqs, per = (B + THREADS - 1) / THREADS;
+  __shared__ int wsum[32];
+  const int threads = blockDim.x, B = a.c.n_seqs, per = (B + threads - 1) / threads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cap = a.c.max_pages << a.c.log2_page;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
   int sum = 0, bad = 0;
   for (int b = b0; b < b1; ++b) {
-    const int n = paged_tiles(paged_visible(paged_length(a.lens[b], cap, &bad), a.window, a.sinks).count);
+    const int n = paged_visible(paged_length(a.lens[b], cap, &bad), a.window, a.sinks).tiles;
     before[b + 1] = n;
     sum += n;
   }
@@ -303,28 +349,31 @@ struct PatWarp;
 // 2^8, exact enough in fp32), so most tiles do not rescale the output.
 template <int HD, int QR>
 struct PatWarp<bf16, HD, QR> {
-  static constexpr int CPR = HD / 8, KS = HD / 16, NT = HD / 8;
+  using S = PatShape<bf16, HD, QR>;
+  static constexpr int KS = HD / 16, NT = HD / 8;
   static constexpr int RV = QR / 8;  // query rows a lane holds statistics of
   uint32_t qf[KS][2 * RV];
   float acc[NT][4];
   float m[RV], l[RV];
 
   __device__ __forceinline__ PatWarp(char*) {}
-  __device__ __forceinline__ void begin(const char* q, int lane) {
+  __device__ __forceinline__ void begin(const char* q, int rows, int lane) {
     const uint32_t qs = smem_u32(q);
-    // rows 0..7 (and 8..15) of Q as first-operand fragments
+    // rows 0..7 (and 8..15) of Q as first-operand fragments; rows that do not exist repeat row 0
+    // and are not written
+    const int mat = lane >> 3, row = lane & 7;
 #pragma unroll
     for (int k = 0; k < KS; k += (RV == 1 ? 2 : 1)) {
       uint32_t r[4];
-      const int mat = lane >> 3, row = lane & 7;
       if constexpr (RV == 1) {  // two k steps: chunks 2k .. 2k + 3 of rows 0..7
-        ldsm_x4(qs + 16 * pat_chunk<CPR>(row, 2 * k + mat), r);
+        ldsm_x4(qs + (row < rows ? row : 0) * S::ROW + 16 * (2 * k + mat), r);
         qf[k][0] = r[0];
         qf[k][1] = r[1];
         qf[k + 1][0] = r[2];
         qf[k + 1][1] = r[3];
       } else {  // rows 0..7, 8..15 at chunk 2k, then at chunk 2k + 1
-        ldsm_x4(qs + 16 * pat_chunk<CPR>(row + 8 * (mat & 1), 2 * k + (mat >> 1)), r);
+        const int at = row + 8 * (mat & 1);
+        ldsm_x4(qs + (at < rows ? at : 0) * S::ROW + 16 * (2 * k + (mat >> 1)), r);
 #pragma unroll
         for (int i = 0; i < 4; ++i) qf[k][i] = r[i];
       }
@@ -343,17 +392,23 @@ struct PatWarp<bf16, HD, QR> {
   __device__ __forceinline__ void tile(const char* kt, const char* vt, uint32_t mask, float scale_log2, int lane) {
     const uint32_t ks = smem_u32(kt), vs = smem_u32(vt);
     const int mat = lane >> 3, row = lane & 7, q = lane & 3;
-    float s[2][4];
+    // even and odd k steps in sums of their own: chains half as long
+    float s[2][4], s2[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = 0.f;
+    for (int i = 0; i < 4; ++i) s[0][i] = s[1][i] = s2[0][i] = s2[1][i] = 0.f;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       uint32_t b[4];  // keys 0..7 at chunks 2k, 2k + 1; keys 8..15 at the same
-      ldsm_x4(ks + 16 * pat_chunk<CPR>(row + 8 * (mat >> 1), 2 * k + (mat & 1)), b);
+      ldsm_x4(ks + S::chunk(row + 8 * (mat >> 1), 2 * k + (mat & 1)), b);
       const uint32_t a1 = RV == 2 ? qf[k][1] : 0u, a3 = RV == 2 ? qf[k][2 * RV - 1] : 0u;
       const uint32_t a2 = RV == 2 ? qf[k][2 * RV - 2] : qf[k][1];
-      dec_mma(s[0], qf[k][0], a1, a2, a3, b[0], b[1]);
-      dec_mma(s[1], qf[k][0], a1, a2, a3, b[2], b[3]);
+      dec_mma(k & 1 ? s2[0] : s[0], qf[k][0], a1, a2, a3, b[0], b[1]);
+      dec_mma(k & 1 ? s2[1] : s[1], qf[k][0], a1, a2, a3, b[2], b[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[0][i] += s2[0][i];
+      s[1][i] += s2[1][i];
     }
     // lane: query row lane / 4 (+ 8), keys 2q, 2q + 1 and 8 + 2q, 9 + 2q
     float p[RV][4];
@@ -409,7 +464,7 @@ struct PatWarp<bf16, HD, QR> {
 #pragma unroll
     for (int j = 0; j < NT; j += 2) {
       uint32_t b[4];  // keys 0..7, 8..15 at chunk j, then at chunk j + 1
-      ldsm_x4_t(vs + 16 * pat_chunk<CPR>(row + 8 * (mat & 1), j + (mat >> 1)), b);
+      ldsm_x4_t(vs + S::chunk(row + 8 * (mat & 1), j + (mat >> 1)), b);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (RV == 1) {
@@ -452,6 +507,7 @@ struct PatWarp<bf16, HD, QR> {
 // or 32 apart for HD 96).
 template <int HD, int QR>
 struct PatWarp<float, HD, QR> {
+  using S = PatShape<float, HD, QR>;
   static constexpr int CPR = HD / 4, E = HD / 32;
   float acc[QR][E];
   float m[QR], l[QR];
@@ -462,10 +518,11 @@ struct PatWarp<float, HD, QR> {
     qb = reinterpret_cast<float4*>(side);
     wb = reinterpret_cast<float*>(side + QR * HD * 4);
   }
-  __device__ __forceinline__ void begin(const char* qs, int lane) {
+  __device__ __forceinline__ void begin(const char* qs, int rows, int lane) {
     // the stage is refilled before the item ends
     const float4* from = reinterpret_cast<const float4*>(qs);
-    for (int i = lane; i < QR * CPR; i += 32) qb[i] = from[pat_chunk<CPR>(i / CPR, i % CPR)];
+    for (int i = lane; i < QR * CPR; i += 32)
+      qb[i] = i < rows * CPR ? from[i] : make_float4(0.f, 0.f, 0.f, 0.f);
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < QR; ++r) {
@@ -477,7 +534,6 @@ struct PatWarp<float, HD, QR> {
   }
 
   __device__ __forceinline__ void tile(const char* ks, const char* vs, uint32_t mask, float scale_log2, int lane) {
-    const float4* kt = reinterpret_cast<const float4*>(ks);
     const int key = lane & 15, half = lane >> 4;
     float s[QR];
 #pragma unroll
@@ -485,7 +541,7 @@ struct PatWarp<float, HD, QR> {
 #pragma unroll 4
     for (int i = 0; i < CPR / 2; ++i) {
       const int c = half * (CPR / 2) + i;
-      const float4 k = kt[pat_chunk<CPR>(key, c)];
+      const float4 k = *reinterpret_cast<const float4*>(ks + S::chunk(key, c));
 #pragma unroll
       for (int r = 0; r < QR; ++r) {
         const float4 q = qb[r * CPR + c];
@@ -512,20 +568,19 @@ struct PatWarp<float, HD, QR> {
       if (half == 0) wb[r * PAT_TILE + key] = p;
     }
     __syncwarp();
-    const float* vt = reinterpret_cast<const float*>(vs);
 #pragma unroll
     for (int k = 0; k < PAT_TILE; k += 4) {
       float v[4][E];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (E == 4) {
-          const float4 x = reinterpret_cast<const float4*>(vt)[pat_chunk<CPR>(k + i, lane)];
+          const float4 x = *reinterpret_cast<const float4*>(vs + S::chunk(k + i, lane));
           v[i][0] = x.x; v[i][1 % E] = x.y; v[i][2 % E] = x.z; v[i][3 % E] = x.w;
         } else {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const int d = E == 2 ? 2 * lane + e : lane + 32 * e;
-            v[i][e] = vt[4 * pat_chunk<CPR>(k + i, d >> 2) + (d & 3)];
+            v[i][e] = *reinterpret_cast<const float*>(vs + S::chunk(k + i, d >> 2) + 4 * (d & 3));
           }
         }
       }
@@ -584,227 +639,336 @@ struct PatOut {
   }
 };
 
-template <class T, int HD, int QR>
-__global__ void __launch_bounds__(PatShape<T, HD, QR>::WARPS * 32, 1)
-    paged_attn_kernel(const PagedAttnArgs a, const PagedAttnPlan pl) {
+// A running join of softmax pieces: o = sum_i o_i 2^(m_i - M), l = sum_i l_i 2^(m_i - M), M =
+// max m_i, of four output elements.
+struct PatSum {
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void add(const float2& ml, const float4& x) {
+    if (ml.x == -INFINITY) return;  // nothing visible in the piece
+    const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), g = exp2f(ml.x - mn);
+    m = mn;
+    l = l * f + ml.y * g;
+    o.x = o.x * f + x.x * g;
+    o.y = o.y * f + x.y * g;
+    o.z = o.z * f + x.z * g;
+    o.w = o.w * f + x.w * g;
+  }
+  template <class T>
+  __device__ __forceinline__ void store(T* to, float* lse) const {
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    to[0] = from_f32<T>(o.x * f);
+    to[1] = from_f32<T>(o.y * f);
+    to[2] = from_f32<T>(o.z * f);
+    to[3] = from_f32<T>(o.w * f);
+    if (lse) *lse = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+  }
+};
+
+// Joins the partial results of an item of `rows` query rows from blocks c0..c1, by the whole
+// block: a thread holds four elements of a row over every parts-th block, with PAJ_AHEAD of them
+// in flight; `scratch` has 24 bytes per thread.
+constexpr int PAJ_AHEAD = 4;
+template <class T, int HD>
+__device__ __forceinline__ void pat_join(const PagedAttnPlan& pl, int c0, int c1, int rows, T* out, float* lse,
+                                         char* scratch) {
+  constexpr int VEC = HD / 4;
+  float4* s_o = reinterpret_cast<float4*>(scratch);
+  float2* s_ml = reinterpret_cast<float2*>(scratch + 16 * blockDim.x);
+  const int cols = rows * VEC, parts = max(1, (int)blockDim.x / cols);
+  for (int col0 = 0; col0 < cols; col0 += blockDim.x) {
+    const int col = col0 + threadIdx.x % cols, p = threadIdx.x / cols;
+    const int row = col / VEC, v = col - row * VEC;
+    PatSum sum;
+    if (p < parts && col < cols) {
+      for (int c = c0 + p; c <= c1; c += parts * PAJ_AHEAD) {
+        float2 ml[PAJ_AHEAD];
+        float4 x[PAJ_AHEAD];
+#pragma unroll
+        for (int j = 0; j < PAJ_AHEAD; ++j) {
+          const int cj = c + j * parts;
+          const int64_t i = ((int64_t)cj * 2 + (cj == c0 ? 1 : 0)) * pl.rows + row;
+          ml[j] = make_float2(-INFINITY, 0.f);
+          if (cj <= c1) {
+            ml[j] = __ldcg(pl.ml + i);
+            x[j] = __ldcg(reinterpret_cast<const float4*>(pl.part + i * HD) + v);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < PAJ_AHEAD; ++j) sum.add(ml[j], x[j]);
+      }
+      s_o[threadIdx.x] = sum.o;
+      s_ml[threadIdx.x] = make_float2(sum.m, sum.l);
+    }
+    __syncthreads();
+    if (p == 0 && col < cols) {
+      for (int i = 1; i < parts; ++i) sum.add(s_ml[threadIdx.x + i * cols], s_o[threadIdx.x + i * cols]);
+      sum.store(out + row * HD + v * 4, lse && v == 0 ? lse + row : nullptr);
+    }
+    __syncthreads();
+  }
+}
+
+template <class T, int HD, int QR, bool BOX>
+__global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
+    paged_attn_kernel(const PagedAttnArgs a, const PagedAttnPlan pl, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
   using S = PatShape<T, HD, QR>;
   constexpr int CPR = S::CPR, STAGES = S::STAGES, VN = 16 / sizeof(T);
-  extern __shared__ __align__(128) char pat_smem[];
-  int* before = reinterpret_cast<int*>(pat_smem + S::WARPS * S::WARP_BYTES);
+  constexpr uint64_t LIMIT_NS = 2000000000ull;  // a wait gives up after two seconds
+  extern __shared__ char pat_raw[];
+  char* pat_smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(pat_raw) + 1023) & ~uintptr_t(1023));
+  // items that are split, for the joins: [0] the one that begins before the block's first
+  // worker, [1 + warp] the one that begins in a warp and does not end there (seq < 0: none)
+  struct Split {
+    int seq, item, tiles;
+    int64_t start;  // its first tile in the order of all tiles
+  };
+  __shared__ Split s_split[S::MAX_WARPS + 1];
+  __shared__ int s_last[2];  // the block is the last to arrive at: the item that comes in, that goes on
+  __shared__ int s_no_abort;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  char* ring = pat_smem + warp * S::WARP_BYTES;
-  uint32_t* masks = reinterpret_cast<uint32_t*>(ring + STAGES * S::STAGE + S::SIDE);
-  pdl_launch_dependents();
-  pat_prefix<S::WARPS * 32>(a, before);
+  char* ring = pat_smem + warp * S::warp_bytes(pl.rows);
+  char* head = ring + S::head(pl.rows);
+  char* side = head + S::piece(pl.rows);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(side + S::SIDE);
+  uint32_t* masks = reinterpret_cast<uint32_t*>(bars + STAGES);
+  int* before = reinterpret_cast<int*>(pat_smem + pl.warps * S::warp_bytes(pl.rows));
+  if (lane == 0) {
+    if (BOX) {
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i) mbar_init(bars + i, 1);
+      fence_barrier_init();
+    }
+    s_split[warp + 1].seq = -1;
+    if (warp == 0) {
+      if (BOX) {
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+      }
+      s_split[0].seq = -1;
+      s_last[0] = s_last[1] = s_no_abort = 0;
+    }
+  }
+  pat_prefix(a, before);
   const int B = a.c.n_seqs;
   // sequences without tokens
   for (int b = blockIdx.x; b < B; b += gridDim.x)
     if (before[b] == before[b + 1])
-      for (int i = threadIdx.x; i < a.nh * HD; i += S::WARPS * 32) {
+      for (int i = threadIdx.x; i < a.nh * HD; i += blockDim.x) {
         static_cast<T*>(a.out)[b * a.ldo + i] = from_f32<T>(0.f);
         if (a.lse && i < a.nh) a.lse[(int64_t)b * a.nh + i] = -INFINITY;
       }
-  const int w = warp * gridDim.x + blockIdx.x;
+  const int w = blockIdx.x * pl.warps + warp;
   const int64_t total = (int64_t)before[B] * pl.items;
-  const int64_t share = paged_share(total, pl.workers, PAT_LEAST);
+  const int64_t share = paged_share(total, pl.workers);
   const int64_t u0 = w * share, u1 = min(total, u0 + share);
-  if (u0 >= u1) {
-    if (lane == 0) pl.rec[2 * w + 1] = -1;
-    return;
-  }
-  const int64_t n = u1 - u0;
-
-  // copies: tile `pc`, whose keys' pages the first 16 lanes have read a tile ahead
-  PagedCursor pc = paged_locate(before, B, pl.items, u0);
-  const PagedCursor first = pc;
-  const int cap = a.c.max_pages << a.c.log2_page, slots = (1 << a.c.log2_page) - 1;
-  int bad = 0, ignore = 0;
-  PagedVisible vis = paged_visible(paged_length(a.lens[pc.seq], cap, &ignore), a.window, a.sinks);
-  int page = 0;
-  auto look_up = [&]() {
-    const int i = pc.tile * PAT_TILE + lane;
-    if (lane < PAT_TILE && i < vis.count)
-      page = a.c.table[pc.seq * a.c.table_stride + (paged_position(vis, i) >> a.c.log2_page)];
-  };
-  auto copy_tile = [&](int stage, bool with_q) {
-    const uint32_t dst = smem_u32(ring + stage * S::STAGE);
-    const int i = pc.tile * PAT_TILE + lane;
-    const bool in = lane < PAT_TILE && i < vis.count;
-    const bool ok = in && (unsigned)page < (unsigned)a.c.n_pages;
-    bad |= in && !ok;
-    const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-    if (lane == 0) masks[stage] = mask;
-    const int hk = pc.item / pl.qtiles;
-    int64_t off = 0;
-    if (ok) off = page * a.c.page_stride + (paged_position(vis, i) & slots) * a.c.row_stride + hk * a.c.head_stride;
-#pragma unroll
-    for (int j = 0; j < PAT_TILE * CPR / 32; ++j) {
-      const int c = lane + 32 * j, row = c / CPR, col = c % CPR;
-      const bool valid = mask >> row & 1;
-      const int64_t o = __shfl_sync(0xffffffffu, (long long)off, row) + (valid ? col * VN : 0);
-      const uint32_t to = dst + 16 * pat_chunk<CPR>(row, col);
-      cp_async_16(to, static_cast<const T*>(a.c.k) + o, valid);
-      cp_async_16(to + PAT_TILE * S::ROW, static_cast<const T*>(a.c.v) + o, valid);
-    }
-    if (with_q) {
-      const int q0 = (pc.item - hk * pl.qtiles) * QR;  // first row of the tile in the group
+  if (u0 < u1) {
+    const int64_t n = u1 - u0;
+    // copies: tile `pc`; the pages of its keys have been read a tile ahead (BOX: the one page, by
+    // all lanes; otherwise the page of key `lane`, by the first 16)
+    PagedCursor pc = paged_locate(before, B, pl.items, u0);
+    const PagedCursor first = pc;
+    const int cap = a.c.max_pages << a.c.log2_page, slots = (1 << a.c.log2_page) - 1;
+    int bad = 0, ignore = 0;
+    PagedVisible vis = paged_visible(paged_length(a.lens[pc.seq], cap, &ignore), a.window, a.sinks);
+    int page = 0, pos = 0;  // of the tile
+    auto look_up = [&]() {
+      pos = paged_tile_pos(vis, pc.tile);
+      const int mine = BOX ? pos : pos + lane;
+      if (BOX || (lane < PAT_TILE && mine < vis.len))
+        page = a.c.table[pc.seq * a.c.table_stride + (mine >> a.c.log2_page)];
+    };
+    auto copy_tile = [&](int stage, bool with_q) {
+      const uint32_t seen = paged_tile_mask(vis, pos);
+      const int hk = pl.qtiles == 1 ? pc.item : pc.item / pl.qtiles;
+      const int q0 = (pc.item - hk * pl.qtiles) * QR, rows = min(QR, pl.group - q0);  // of the group
       const T* q = static_cast<const T*>(a.q) + pc.seq * a.ldq + (hk * pl.group + q0) * HD;
-      for (int c = lane; c < QR * CPR; c += 32) {
-        const int row = c / CPR, col = c % CPR;
-        const bool valid = q0 + row < pl.group;
-        cp_async_16(dst + S::QOFF + 16 * pat_chunk<CPR>(row, col), valid ? q + row * HD + col * VN : a.q, valid);
-      }
-    }
-  };
-  auto forward = [&]() {
-    if (paged_next(pc, before, pl.items))
-      vis = paged_visible(paged_length(a.lens[pc.seq], cap, &ignore), a.window, a.sinks);
-    look_up();
-  };
-  look_up();
+      char* qs = ring + S::RING + stage * pl.rows * S::ROW;
+      char* ks = ring + stage * 2 * S::TILE;
+      if constexpr (BOX) {
+        const bool ok = (unsigned)page < (unsigned)a.c.n_pages;
+        bad |= !ok;
+        if (lane == 0) {
+          masks[stage] = ok ? seen : 0u;
+          const uint32_t bytes = (ok ? 2 * S::TILE : 0) + (with_q ? rows * S::ROW : 0);
+          if (bytes)
+            mbar_arrive_expect_tx(bars + stage, bytes);
+          else
+            mbar_arrive(bars + stage);
+          if (ok) {
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s) {
-    if (s < n) {
-      copy_tile(s, s == 0 || pc.tile == 0);
-      if (s + 1 < n) forward();
-    }
-    cp_async_commit();
-  }
-
-  PagedCursor c = first;
-  const float scale_log2 = a.scale * 1.4426950408889634f;
-  PatWarp<T, HD, QR> pw(ring + STAGES * S::STAGE);
-  int stage = 0, from = 0, split = -1;
-  for (int64_t t = 0; t < n; ++t) {
-    cp_async_wait<STAGES - 2>();
-    __syncwarp();
-    if (t + STAGES - 1 < n) {
-      copy_tile(stage == 0 ? STAGES - 1 : stage - 1, pc.tile == 0);
-      if (t + STAGES < n) forward();
-    }
-    cp_async_commit();
-    const char* buf = ring + stage * S::STAGE;
-    if (t == 0 || c.tile == 0) {
-      pw.begin(buf + S::QOFF, lane);
-      from = c.tile;
-    }
-    pw.tile(buf, buf + PAT_TILE * S::ROW, masks[stage], scale_log2, lane);
-    const bool end = c.tile == c.tiles - 1;
-    if (end || t == n - 1) {
-      const int hk = c.item / pl.qtiles, q0 = (c.item - hk * pl.qtiles) * QR, h = hk * pl.group + q0;
-      const bool whole = end && from == 0;
-      const int64_t slot = ((int64_t)w * 2 + (end ? 0 : 1)) * pl.rows;
-      PatOut<T> out;
-      out.rows = min(QR, pl.group - q0);
-      out.out = whole ? static_cast<T*>(a.out) + c.seq * a.ldo + h * HD : nullptr;
-      out.lse = a.lse ? a.lse + (int64_t)c.seq * a.nh + h : nullptr;
-      out.part = pl.part + slot * HD;
-      out.ml = pl.ml + slot;
-      out.hd = HD;
-      pw.finish(lane, out);
-      if (!end && from == 0) split = c.seq * pl.items + c.item;
-    }
-    if (t + 1 < n) paged_next(c, before, pl.items);
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-  }
-  cp_async_wait<0>();
-  if (bad) raise_device_error(a.c.status, DEV_PAGE_RANGE);
-  if (lane == 0) {
-    // the item that this worker begins and does not end: its last tile's worker
-    int last = -1;
-    if (split >= 0) {
-      const int64_t end = u1 + (c.tiles - 1 - c.tile);  // c is still at tile u1 - 1
-      last = (int)((end - 1) / share);
-      pl.rec[2 * w] = split;
-    }
-    pl.rec[2 * w + 1] = last;
-  }
-}
-
-// Joins the partial results of the items that begin in workers 8 blockIdx.x ... + 7 and go on in
-// later ones: o = sum_i o_i 2^(m_i - M) / sum_i l_i 2^(m_i - M), M = max m_i. A block does the
-// rows blockIdx.y, + gridDim.y, ...; a thread holds four output elements over every PARTS-th
-// partial result, with the loads of PAJ_AHEAD of them in flight.
-constexpr int PAJ_THREADS = 256, PAJ_WORKERS = 8, PAJ_AHEAD = 4;
-template <class T, int HD>
-__global__ void __launch_bounds__(PAJ_THREADS) paged_join_kernel(const PagedAttnArgs a, const PagedAttnPlan pl, int qr) {
-  constexpr int VEC = HD / 4, PARTS = PAJ_THREADS / VEC;
-  __shared__ float4 s_o[PARTS][VEC];
-  __shared__ float2 s_ml[PARTS];
-  __shared__ int2 s_rec[PAJ_WORKERS];
-  pdl_wait();
-  const int base = blockIdx.x * PAJ_WORKERS;
-  if (threadIdx.x < PAJ_WORKERS)
-    s_rec[threadIdx.x] =
-        base + (int)threadIdx.x < pl.workers ? *reinterpret_cast<const int2*>(pl.rec + 2 * (base + threadIdx.x)) : make_int2(0, -1);
-  __syncthreads();
-  const int v = threadIdx.x % VEC, p = threadIdx.x / VEC;
-  for (int k = 0; k < PAJ_WORKERS; ++k) {
-    const int w0 = base + k, w1 = s_rec[k].y;
-    if (w1 < 0) continue;
-    const int id = s_rec[k].x, b = id / pl.items, item = id - b * pl.items;
-    const int hk = item / pl.qtiles, q0 = (item - hk * pl.qtiles) * qr, rows = min(qr, pl.group - q0);
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-      if (p < PARTS) {
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = w0 + p; w <= w1; w += PARTS * PAJ_AHEAD) {
-          float2 ml[PAJ_AHEAD];
-          float4 x[PAJ_AHEAD];
-#pragma unroll
-          for (int j = 0; j < PAJ_AHEAD; ++j) {
-            const int wj = w + j * PARTS;
-            const int64_t i = ((int64_t)wj * 2 + (wj == w1 ? 0 : 1)) * pl.rows + r;
-            ml[j] = make_float2(-INFINITY, 0.f);
-            if (wj <= w1) {
-              ml[j] = pl.ml[i];
-              x[j] = *reinterpret_cast<const float4*>(pl.part + i * HD + v * 4);
+            for (int i = 0; i < S::BOXES; ++i) {
+              const int x = i * (S::BOX_ROW / (int)sizeof(T));
+              tma_load_4d(ks + i * S::BOX, &kmap, bars + stage, x, pos & slots, hk, page);
+              tma_load_4d(ks + S::TILE + i * S::BOX, &vmap, bars + stage, x, pos & slots, hk, page);
             }
           }
+          if (with_q) bulk_load_1d(qs, q, rows * S::ROW, bars + stage);
+        }
+      } else {
+        const bool in = lane < PAT_TILE && (seen >> lane & 1);
+        const bool ok = in && (unsigned)page < (unsigned)a.c.n_pages;
+        bad |= in && !ok;
+        const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0) masks[stage] = mask;
+        int64_t off = 0;
+        if (ok) off = page * a.c.page_stride + ((pos + lane) & slots) * a.c.row_stride + hk * a.c.head_stride;
+        const uint32_t dst = smem_u32(ks);
 #pragma unroll
-          for (int j = 0; j < PAJ_AHEAD; ++j) {
-            const float mn = fmaxf(m, ml[j].x);
-            if (ml[j].x == -INFINITY) continue;  // past the end, or nothing visible in the piece
-            const float f = exp2f(m - mn), g = exp2f(ml[j].x - mn);
-            m = mn;
-            l = l * f + ml[j].y * g;
-            o.x = o.x * f + x[j].x * g;
-            o.y = o.y * f + x[j].y * g;
-            o.z = o.z * f + x[j].z * g;
-            o.w = o.w * f + x[j].w * g;
-          }
+        for (int j = 0; j < PAT_TILE * CPR / 32; ++j) {
+          const int c = lane + 32 * j, row = c / CPR, col = c % CPR;
+          const bool valid = mask >> row & 1;
+          const int64_t o = __shfl_sync(0xffffffffu, (long long)off, row) + (valid ? col * VN : 0);
+          const uint32_t to = dst + S::chunk(row, col);
+          cp_async_16(to, static_cast<const T*>(a.c.k) + o, valid);
+          cp_async_16(to + S::TILE, static_cast<const T*>(a.c.v) + o, valid);
         }
-        s_o[p][v] = o;
-        if (v == 0) s_ml[p] = make_float2(m, l);
+        if (with_q)
+          for (int c = lane; c < rows * CPR; c += 32) cp_async_16(smem_u32(qs) + 16 * c, q + c * VN, true);
       }
-      __syncthreads();
-      if (p == 0) {
-        float M = -INFINITY;
-        for (int i = 0; i < PARTS; ++i) M = fmaxf(M, s_ml[i].x);
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < PARTS; ++i) {
-          const float2 ml = s_ml[i];
-          if (ml.x == -INFINITY) continue;
-          const float g = exp2f(ml.x - M);
-          const float4 x = s_o[i][v];
-          l += ml.y * g;
-          o.x += x.x * g;
-          o.y += x.y * g;
-          o.z += x.z * g;
-          o.w += x.w * g;
-        }
-        const float f = l == 0.f ? 0.f : 1.f / l;
-        const int h = hk * pl.group + q0 + r;
-        T* out = static_cast<T*>(a.out) + b * a.ldo + h * HD + v * 4;
-        out[0] = from_f32<T>(o.x * f);
-        out[1] = from_f32<T>(o.y * f);
-        out[2] = from_f32<T>(o.z * f);
-        out[3] = from_f32<T>(o.w * f);
-        if (a.lse && v == 0) a.lse[(int64_t)b * a.nh + h] = l == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(l);
+    };
+    auto forward = [&]() {
+      if (paged_next(pc, before, pl.items))
+        vis = paged_visible(paged_length(a.lens[pc.seq], cap, &ignore), a.window, a.sinks);
+      look_up();
+    };
+    look_up();
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+      if (s < n) {
+        copy_tile(s, s == 0 || pc.tile == 0);
+        if (s + 1 < n) forward();
       }
-      __syncthreads();
+      if (!BOX) cp_async_commit();
     }
+
+    PagedCursor c = first;
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    PatWarp<T, HD, QR> pw(side);
+    int stage = 0, from = 0;
+    uint32_t parity = 0;
+    bool dead = false;
+    for (int64_t t = 0; t < n; ++t) {
+      if constexpr (BOX) {
+        const bool ok = dead || mbar_wait_bounded(bars + stage, parity, &s_no_abort, LIMIT_NS);
+        if (__any_sync(0xffffffffu, !ok)) {
+          // a copy did not arrive: no more copies and waits, the result is void and reported; the
+          // copies in flight are waited for once more, so that none outlives the block
+          dead = true;
+          bad = 2;
+          for (int i = 0; i < STAGES && t + i < n; ++i) {
+            const int s = stage + i < STAGES ? stage + i : stage + i - STAGES;
+            mbar_wait_bounded(bars + s, stage + i < STAGES ? parity : parity ^ 1u, &s_no_abort, LIMIT_NS);
+          }
+          __syncwarp();
+        }
+      } else {
+        cp_async_wait<STAGES - 1>();
+        __syncwarp();
+      }
+      char* ks = ring + stage * 2 * S::TILE;
+      const uint32_t mask = masks[stage];
+      if (BOX && mask != 0xffffu) {
+        // what a page holds in place of unseen keys may be anything: their weights are 0, and
+        // their values must not be infinite or NaN
+        for (int i = lane; i < PAT_TILE * CPR; i += 32)
+          if (!(mask >> (i / CPR) & 1))
+            *reinterpret_cast<uint4*>(ks + S::TILE + S::chunk(i / CPR, i % CPR)) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();  // before the next copy into this stage
+        __syncwarp();
+      }
+      if (t == 0 || c.tile == 0) {
+        pw.begin(ring + S::RING + stage * pl.rows * S::ROW, pl.rows, lane);
+        from = c.tile;
+      }
+      pw.tile(ks, ks + S::TILE, mask, scale_log2, lane);
+      __syncwarp();
+      if (t + STAGES < n && !dead) {
+        copy_tile(stage, pc.tile == 0);
+        if (t + STAGES + 1 < n) forward();
+      }
+      if (!BOX) cp_async_commit();
+      const bool end = c.tile == c.tiles - 1;
+      if (end || t == n - 1) {
+        const int hk = c.item / pl.qtiles, q0 = (c.item - hk * pl.qtiles) * QR, h = hk * pl.group + q0;
+        const bool whole = end && from == 0;
+        // the tail piece goes to the ring, which is done with
+        char* piece = from == 0 ? ring : head;
+        PatOut<T> out;
+        out.rows = min(QR, pl.group - q0);
+        out.out = whole ? static_cast<T*>(a.out) + c.seq * a.ldo + h * HD : nullptr;
+        out.lse = a.lse ? a.lse + (int64_t)c.seq * a.nh + h : nullptr;
+        out.part = reinterpret_cast<float*>(piece);
+        out.ml = reinterpret_cast<float2*>(piece + pl.rows * HD * 4);
+        out.hd = HD;
+        pw.finish(lane, out);
+        if (!whole && lane == 0) {
+          const Split sp{c.seq, c.item, c.tiles, u0 + t - c.tile};
+          if (from > 0 && warp == 0) s_split[0] = sp;
+          if (from == 0) s_split[warp + 1] = sp;
+        }
+      }
+      if (t + 1 < n) paged_next(c, before, pl.items);
+      if (++stage == STAGES) {
+        stage = 0;
+        parity ^= 1u;
+      }
+    }
+    if (!BOX) cp_async_wait<0>();
+    if (bad) raise_device_error(a.c.status, bad == 2 ? DEV_TIMEOUT : DEV_PAGE_RANGE);
+  }
+  __syncthreads();
+  // warp k joins the item that begins in it; the last warp also the one that comes in
+  const int wb = blockIdx.x * pl.warps, we = wb + pl.warps - 1;  // the block's workers
+  auto place = [&](const Split& sp, int& w0, int& w1, int& h, int& rows) {
+    w0 = (int)paged_div(sp.start, share);
+    w1 = (int)paged_div(sp.start + sp.tiles - 1, share);
+    const int hk = sp.item / pl.qtiles, q0 = (sp.item - hk * pl.qtiles) * QR;
+    h = hk * pl.group + q0;
+    rows = min(QR, pl.group - q0);
+  };
+  for (int k = warp == pl.warps - 1 ? 0 : warp + 1; k <= warp + 1; k += warp + 1) {
+    const Split sp = s_split[k];
+    if (sp.seq < 0) continue;
+    int w0, w1, h, rows;
+    place(sp, w0, w1, h, rows);
+    const bool inside = k > 0 && w1 <= we;
+    T* out = static_cast<T*>(a.out) + sp.seq * a.ldo + h * HD;
+    float* lse = a.lse ? a.lse + (int64_t)sp.seq * a.nh + h : nullptr;
+    const int64_t slot = ((int64_t)blockIdx.x * 2 + (k > 0 ? 1 : 0)) * pl.rows;
+    const int p0 = max(w0, wb) - wb, p1 = min(w1, we) - wb;  // the warps with a piece
+    constexpr int VEC = HD / 4;
+    for (int col = lane; col < rows * VEC; col += 32) {
+      const int row = col / VEC, v = col - row * VEC;
+      PatSum sum;
+      for (int p = p0; p <= p1; ++p) {
+        const char* piece = pat_smem + p * S::warp_bytes(pl.rows) + (k > 0 && p == p0 ? 0 : S::head(pl.rows));
+        sum.add(reinterpret_cast<const float2*>(piece + pl.rows * HD * 4)[row], reinterpret_cast<const float4*>(piece)[col]);
+      }
+      if (inside) {
+        sum.store(out + col * 4, lse && v == 0 ? lse + row : nullptr);
+      } else {
+        reinterpret_cast<float4*>(pl.part + slot * HD)[col] = sum.o;
+        if (v == 0) pl.ml[slot + row] = make_float2(sum.m, sum.l);
+      }
+    }
+    if (!inside) {
+      __syncwarp();
+      if (lane == 0) s_last[k > 0] = pat_arrive(pl.arrived + w0 / pl.warps, pl.tag, w1 / pl.warps - w0 / pl.warps + 1);
+    }
+  }
+  __syncthreads();
+  for (int i = 0; i < 2; ++i) {
+    if (!s_last[i]) continue;
+    int k = 0;  // the item that goes on begins in the last worker with a tail piece
+    if (i == 1)
+      for (k = pl.warps; s_split[k].seq < 0;) --k;
+    const Split sp = s_split[k];
+    int w0, w1, h, rows;
+    place(sp, w0, w1, h, rows);
+    pat_join<T, HD>(pl, w0 / pl.warps, w1 / pl.warps, rows, static_cast<T*>(a.out) + sp.seq * a.ldo + h * HD,
+                    a.lse ? a.lse + (int64_t)sp.seq * a.nh + h : nullptr, pat_smem);
   }
 }
 

@@ -12,25 +12,40 @@
 
 namespace g2 {
 
-// The tokens that the newest of `len` tokens sees, as positions: the first `sink`, then the
-// contiguous range that ends at len - 1. The i-th visible token (0 <= i < count) is at
-// position i for i < sink and i + shift otherwise.
+// The work of one attention call is cut into tiles of PAT_TILE keys at positions 16 i ... 16 i +
+// 15: with pages of 16 tokens or more a tile lies in one page.
+constexpr int PAT_TILE = 16;
+
+// The tokens that the newest of `len` tokens sees: positions below `sink` and lo .. len - 1; and
+// the tiles that hold them: the first `sink_tiles`, then those from `first` on, `tiles` in all.
 struct PagedVisible {
-  int sink, shift, count;
+  int len, lo, sink, sink_tiles, first, tiles;
 };
 
 // len tokens cached, of which the newest has just been appended; window <= 0: all of them
 // are visible; otherwise the newest `window`, and the first `sinks` besides.
 G2_HD PagedVisible paged_visible(int len, int window, int sinks) {
   PagedVisible v;
-  const int lo = window > 0 && len > window ? len - window : 0;
-  v.sink = sinks < lo ? sinks : lo;
-  v.shift = lo - v.sink;
-  v.count = len - v.shift;
+  v.len = len;
+  v.lo = window > 0 && len > window ? len - window : 0;
+  v.sink = sinks < v.lo ? sinks : v.lo;
+  v.sink_tiles = v.sink / PAT_TILE + (v.sink % PAT_TILE != 0);
+  const int at = v.lo / PAT_TILE;
+  v.first = at > v.sink_tiles ? at : v.sink_tiles;
+  v.tiles = len > 0 ? v.sink_tiles + (len - 1) / PAT_TILE - v.first + 1 : 0;
   return v;
 }
 
-G2_HD int paged_position(const PagedVisible& v, int i) { return i < v.sink ? i : i + v.shift; }
+// The position of the first key of tile `t` (0 <= t < tiles), and which of its 16 keys are seen.
+G2_HD int paged_tile_pos(const PagedVisible& v, int t) {
+  return (t < v.sink_tiles ? t : t - v.sink_tiles + v.first) * PAT_TILE;
+}
+G2_HD uint32_t paged_below(int n) {  // bits 0 .. n - 1 of 16
+  return n <= 0 ? 0u : n >= PAT_TILE ? 0xffffu : (1u << n) - 1;
+}
+G2_HD uint32_t paged_tile_mask(const PagedVisible& v, int pos) {
+  return (paged_below(v.len - pos) & ~paged_below(v.lo - pos)) | paged_below(v.sink - pos);
+}
 
 // A sequence length as read from device memory, brought into [0, capacity]; *bad is set when
 // it was outside.
@@ -42,14 +57,14 @@ G2_HD int paged_length(int len, int capacity, int* bad) {
   return len;
 }
 
-// The work of one attention call is cut into tiles of PAT_TILE visible keys of one item (a
-// sequence, a key head and a tile of its query heads), laid end to end: sequence by sequence,
-// item by item. Worker w takes tiles [w * share, (w + 1) * share).
-constexpr int PAT_TILE = 16;
-G2_HD int paged_tiles(int count) { return (count + PAT_TILE - 1) / PAT_TILE; }
-G2_HD int64_t paged_share(int64_t total, int workers, int least) {
-  const int64_t s = (total + workers - 1) / workers;
-  return s < least ? least : s;
+// The tiles of all items (a sequence, a key head and a tile of its query heads) are laid end to
+// end: sequence by sequence, item by item. Worker w takes tiles [w * share, (w + 1) * share).
+G2_HD int64_t paged_div(int64_t x, int64_t d) {  // 0 <= x, 1 <= d; nearly always 32-bit numbers
+  return ((x | d) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
+}
+G2_HD int64_t paged_share(int64_t total, int workers) {
+  const int64_t s = paged_div(total + workers - 1, workers);
+  return s < 1 ? 1 : s;
 }
 
 // A place in that order: tile `tile` (of `tiles`) of item `item` (of `items`) of sequence
@@ -60,7 +75,7 @@ struct PagedCursor {
 
 // The place of tile u of the whole order, 0 <= u < items * before[n_seqs].
 G2_HD PagedCursor paged_locate(const int* before, int n_seqs, int items, int64_t u) {
-  const int r = (int)(u / items);  // the sequence with before[seq] <= r < before[seq + 1]
+  const int r = (int)paged_div(u, items);  // the sequence with before[seq] <= r < before[seq + 1]
   int lo = 0, hi = n_seqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -73,7 +88,7 @@ G2_HD PagedCursor paged_locate(const int* before, int n_seqs, int items, int64_t
   c.seq = lo;
   c.tiles = before[lo + 1] - before[lo];
   const int64_t v = u - (int64_t)before[lo] * items;
-  c.item = (int)(v / c.tiles);
+  c.item = (int)paged_div(v, c.tiles);
   c.tile = (int)(v - (int64_t)c.item * c.tiles);
   return c;
 }
