@@ -1218,16 +1218,16 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedApp
 
 inline bool paged_heads_ok(int nh, int nkv) { return nkv >= 1 && nh >= 1 && nh <= 4096 && nh % nkv == 0; }
 
-// Partial results of at most PAT_MAX_BLOCKS blocks: two each, of min(16, group) rows; and an
-// arrival word each.
+// Partial results of at most PAT_MAX_BLOCKS blocks: two each, of min(16, group) rows, with a
+// flag.
 inline size_t paged_attention_ws_bytes(int n_seqs, int nh, int nkv, int hd) {
   if (n_seqs < 0 || n_seqs > PAGED_MAX_SEQS || !paged_heads_ok(nh, nkv) || hd < 1 || hd > 128) return 0;
   const size_t rows = std::min(16, nh / nkv);
-  return (size_t)PAT_MAX_BLOCKS * (8 + 2 * rows * (8 + (size_t)hd * 4));
+  return (size_t)PAT_MAX_BLOCKS * 2 * (8 + rows * (8 + (size_t)hd * 4));
 }
 
 // A number that no other call of this process has, and that what a workspace happens to hold
-// does not have either (48 random bits of it would have to agree).
+// does not have either (64 bits would have to agree).
 inline unsigned long long paged_call_tag() {
   static std::atomic<unsigned long long> next{
       (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() ^
@@ -1236,7 +1236,7 @@ inline unsigned long long paged_call_tag() {
   z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
   z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
   z ^= z >> 31;
-  return (z | (1ull << 63)) & ~((1ull << PAT_COUNT_BITS) - 1);
+  return z | 1;  // not 0, a clear flag
 }
 
 // A pool as a 4-D tensor {head_dim, page_size, n_kv_heads, n_pages}; box: 16 tokens of one head
@@ -1288,7 +1288,7 @@ int paged_attention_inst(const LaunchCtx& c, const gpt2_paged_kv* kv, const Page
   p += (size_t)grid * 2 * pl.rows * HD * 4;
   pl.ml = reinterpret_cast<float2*>(p);
   p += (size_t)grid * 2 * pl.rows * 8;
-  pl.arrived = reinterpret_cast<unsigned long long*>(p);
+  pl.flags = reinterpret_cast<unsigned long long*>(p);
   const cudaError_t e = launch_k(c, paged_attn_kernel<T, HD, QR, BOX>, dim3(grid), dim3(pl.warps * 32),
                                  S::smem(pl.rows, a.c.n_seqs), a, pl, km, vm);
   if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_attention: ") + cudaGetErrorString(e));

@@ -252,32 +252,36 @@ struct PatShape {
 struct PagedAttnPlan {
   int warps;    // of a block
   int workers, items, qtiles, group, rows;  // rows: min(QR, group), the rows of a partial result
-  unsigned long long tag;                   // of this call, in the bits above PAT_COUNT_BITS
-  unsigned long long* arrived;              // [blocks]: see pat_arrive
+  unsigned long long tag;                   // of this call
+  unsigned long long* flags;                // [blocks][2]: see pat_arrive
   float2* ml;                               // [blocks][2][rows]: maximum (log2 units) and sum
   float* part;                              // [blocks][2][rows][HD]
 };
 
-// Counts the blocks that have finished their part of one item in the word of its first block;
-// true for the n-th. A word belongs to this call only while it carries the call's tag, so it may
-// hold anything before the first arrival; the last one clears it, so that a captured call may run
-// again with the same tag.
-constexpr int PAT_COUNT_BITS = 16;
-__device__ __forceinline__ bool pat_arrive(unsigned long long* word, unsigned long long tag, int n) {
-  unsigned long long old = 0;  // what the last call that used the word has left
-  for (;;) {
-    const bool mine = (old >> PAT_COUNT_BITS) == (tag >> PAT_COUNT_BITS);
-    const int count = (mine ? (int)(old & ((1 << PAT_COUNT_BITS) - 1)) : 0) + 1;
-    const unsigned long long next = count == n ? 0ull : tag | (unsigned)count;
-    unsigned long long seen;
-    // releases this block's partial result, acquires those of the blocks that arrived before
-    asm volatile("atom.acq_rel.gpu.global.cas.b64 %0, [%1], %2, %3;"
-                 : "=l"(seen)
-                 : "l"(word), "l"(old), "l"(next)
-                 : "memory");
-    if (seen == old) return count == n;
-    old = seen;  // another block arrived in between: at most n - 1 times
+// The blocks b0..b1 that share an item each set a flag when their partial result is in the
+// workspace, then look at all of them; whoever sees them all set joins the item and clears them.
+// The fence between setting and looking makes at least one block see all (the one whose fence is
+// last); if two do, both write the same output. A flag is set when it holds the call's tag, so
+// the flags may hold anything before a call; they are clear after it, so that a captured call
+// may run again with the same tag. No block waits for another, and no atomic is contended (a
+// counter with compare-and-swap took a microsecond per block that arrived at the same time).
+// One warp calls this, after a barrier behind the block's writes.
+__device__ __forceinline__ bool pat_arrive(unsigned long long* flags, unsigned long long tag, int b0, int b1) {
+  const int lane = threadIdx.x & 31;
+  // a block's flag of the item that begins in it is its second
+  if (lane == 0) {
+    __threadfence();
+    *reinterpret_cast<volatile unsigned long long*>(flags + 2 * blockIdx.x + ((int)blockIdx.x == b0)) = tag;
   }
+  __syncwarp();
+  asm volatile("fence.sc.gpu;" ::: "memory");
+  bool all = true;
+  for (int b = b0 + lane; b <= b1; b += 32)
+    all &= *reinterpret_cast<volatile unsigned long long*>(flags + 2 * b + (b == b0)) == tag;
+  if (!__all_sync(0xffffffffu, all)) return false;
+  __threadfence();
+  for (int b = b0 + lane; b <= b1; b += 32) flags[2 * b + (b == b0)] = 0ull;
+  return true;
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
@@ -639,48 +643,68 @@ struct PatOut {
   }
 };
 
-// A running join of softmax pieces: o = sum_i o_i 2^(m_i - M), l = sum_i l_i 2^(m_i - M), M =
-// max m_i, of four output elements.
+// A join of softmax pieces: o = sum_i o_i 2^(m_i - M), l = sum_i l_i 2^(m_i - M), M = max m_i, of
+// four output elements. Pieces are added N at a time: one rescaling for all of them.
 struct PatSum {
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  __device__ __forceinline__ void add(const float2& ml, const float4& x) {
-    if (ml.x == -INFINITY) return;  // nothing visible in the piece
-    const float mn = fmaxf(m, ml.x), f = exp2f(m - mn), g = exp2f(ml.x - mn);
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&x)[N]) {
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) mn = fmaxf(mn, ml[i].x);
+    if (mn == -INFINITY) return;  // nothing visible so far
+    const float f = ex2_fast(m - mn);
     m = mn;
-    l = l * f + ml.y * g;
-    o.x = o.x * f + x.x * g;
-    o.y = o.y * f + x.y * g;
-    o.z = o.z * f + x.z * g;
-    o.w = o.w * f + x.w * g;
+    l *= f;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float g = ex2_fast(ml[i].x - mn);
+      l = fmaf(ml[i].y, g, l);
+      o.x = fmaf(x[i].x, g, o.x);
+      o.y = fmaf(x[i].y, g, o.y);
+      o.z = fmaf(x[i].z, g, o.z);
+      o.w = fmaf(x[i].w, g, o.w);
+    }
   }
-  template <class T>
-  __device__ __forceinline__ void store(T* to, float* lse) const {
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    to[0] = from_f32<T>(o.x * f);
-    to[1] = from_f32<T>(o.y * f);
-    to[2] = from_f32<T>(o.z * f);
-    to[3] = from_f32<T>(o.w * f);
+  __device__ __forceinline__ void store(bf16* to, float* lse) const {
+    const float f = scale(lse);
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+  }
+  __device__ __forceinline__ void store(float* to, float* lse) const {
+    const float f = scale(lse);
+    *reinterpret_cast<float4*>(to) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  }
+  __device__ __forceinline__ float scale(float* lse) const {
     if (lse) *lse = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    return l == 0.f ? 0.f : 1.f / l;
   }
 };
 
-// Joins the partial results of an item of `rows` query rows from blocks c0..c1, by the whole
-// block: a thread holds four elements of a row over every parts-th block, with PAJ_AHEAD of them
-// in flight; `scratch` has 24 bytes per thread.
+// Joins the partial results of an item of `rows` query rows from blocks c0..c1 by `threads`
+// threads, t = 0 ... threads - 1: a thread holds four elements of a row over every parts-th
+// block, with PAJ_AHEAD of them in flight. All threads of the block go through the barriers of
+// `rounds` rounds; `scratch` has 24 bytes per thread.
 constexpr int PAJ_AHEAD = 4;
 template <class T, int HD>
 __device__ __forceinline__ void pat_join(const PagedAttnPlan& pl, int c0, int c1, int rows, T* out, float* lse,
-                                         char* scratch) {
+                                         char* scratch, int t, int threads, int rounds) {
   constexpr int VEC = HD / 4;
   float4* s_o = reinterpret_cast<float4*>(scratch);
   float2* s_ml = reinterpret_cast<float2*>(scratch + 16 * blockDim.x);
-  const int cols = rows * VEC, parts = max(1, (int)blockDim.x / cols);
-  for (int col0 = 0; col0 < cols; col0 += blockDim.x) {
-    const int col = col0 + threadIdx.x % cols, p = threadIdx.x / cols;
+  const int cols = rows * VEC, n = c1 - c0 + 1;
+  // the same for a whole and a half block, so that sums do not depend on who joins
+  const int parts = max(1, min((int)blockDim.x / 2 / cols, (n + PAJ_AHEAD - 1) / PAJ_AHEAD));
+  for (int k = 0; k < rounds; ++k) {
+    const int p = cols <= threads ? t / cols : 0, col = cols <= threads ? t - p * cols : k * threads + t;
+    const bool mine = t < threads && p < parts && col < cols;
     const int row = col / VEC, v = col - row * VEC;
     PatSum sum;
-    if (p < parts && col < cols) {
+    if (mine) {
       for (int c = c0 + p; c <= c1; c += parts * PAJ_AHEAD) {
         float2 ml[PAJ_AHEAD];
         float4 x[PAJ_AHEAD];
@@ -689,20 +713,24 @@ __device__ __forceinline__ void pat_join(const PagedAttnPlan& pl, int c0, int c1
           const int cj = c + j * parts;
           const int64_t i = ((int64_t)cj * 2 + (cj == c0 ? 1 : 0)) * pl.rows + row;
           ml[j] = make_float2(-INFINITY, 0.f);
+          x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (cj <= c1) {
             ml[j] = __ldcg(pl.ml + i);
             x[j] = __ldcg(reinterpret_cast<const float4*>(pl.part + i * HD) + v);
           }
         }
-#pragma unroll
-        for (int j = 0; j < PAJ_AHEAD; ++j) sum.add(ml[j], x[j]);
+        sum.add(ml, x);
       }
       s_o[threadIdx.x] = sum.o;
       s_ml[threadIdx.x] = make_float2(sum.m, sum.l);
     }
     __syncthreads();
-    if (p == 0 && col < cols) {
-      for (int i = 1; i < parts; ++i) sum.add(s_ml[threadIdx.x + i * cols], s_o[threadIdx.x + i * cols]);
+    if (mine && p == 0) {
+      for (int i = 1; i < parts; ++i) {
+        const float2 ml[1] = {s_ml[threadIdx.x + i * cols]};
+        const float4 x[1] = {s_o[threadIdx.x + i * cols]};
+        sum.add(ml, x);
+      }
       sum.store(out + row * HD + v * 4, lse && v == 0 ? lse + row : nullptr);
     }
     __syncthreads();
@@ -721,11 +749,12 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   // items that are split, for the joins: [0] the one that begins before the block's first
   // worker, [1 + warp] the one that begins in a warp and does not end there (seq < 0: none)
   struct Split {
-    int seq, item, tiles;
-    int64_t start;  // its first tile in the order of all tiles
+    int seq, w0, w1;  // its workers, over all blocks
+    int h, rows;      // its query heads
   };
   __shared__ Split s_split[S::MAX_WARPS + 1];
-  __shared__ int s_last[2];  // the block is the last to arrive at: the item that comes in, that goes on
+  __shared__ int s_cross[2];  // which of them other blocks share: the one that comes in, that goes on (-1: none)
+  __shared__ int s_last[2];   // this block is the last to arrive at it
   __shared__ int s_no_abort;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   char* ring = pat_smem + warp * S::warp_bytes(pl.rows);
@@ -747,6 +776,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
         tma_prefetch_desc(&vmap);
       }
       s_split[0].seq = -1;
+      s_cross[0] = s_cross[1] = -1;
       s_last[0] = s_last[1] = s_no_abort = 0;
     }
   }
@@ -759,7 +789,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
         static_cast<T*>(a.out)[b * a.ldo + i] = from_f32<T>(0.f);
         if (a.lse && i < a.nh) a.lse[(int64_t)b * a.nh + i] = -INFINITY;
       }
-  const int w = blockIdx.x * pl.warps + warp;
+  const int wb = blockIdx.x * pl.warps, we = wb + pl.warps - 1, w = wb + warp;  // the block's workers
   const int64_t total = (int64_t)before[B] * pl.items;
   const int64_t share = paged_share(total, pl.workers);
   const int64_t u0 = w * share, u1 = min(total, u0 + share);
@@ -903,10 +933,12 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
         out.ml = reinterpret_cast<float2*>(piece + pl.rows * HD * 4);
         out.hd = HD;
         pw.finish(lane, out);
-        if (!whole && lane == 0) {
-          const Split sp{c.seq, c.item, c.tiles, u0 + t - c.tile};
-          if (from > 0 && warp == 0) s_split[0] = sp;
-          if (from == 0) s_split[warp + 1] = sp;
+        if (!whole && lane == 0 && (from == 0 || warp == 0)) {
+          const int64_t start = u0 + t - c.tile;  // the item's first tile
+          const int k = from == 0 ? warp + 1 : 0, w0 = from == 0 ? w : (int)paged_div(start, share);
+          const int w1 = (int)paged_div(start + c.tiles - 1, share);
+          s_split[k] = Split{c.seq, w0, w1, h, out.rows};
+          if (k == 0 || w1 > we) s_cross[k > 0] = k;
         }
       }
       if (t + 1 < n) paged_next(c, before, pl.items);
@@ -918,58 +950,59 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
     if (!BOX) cp_async_wait<0>();
     if (bad) raise_device_error(a.c.status, bad == 2 ? DEV_TIMEOUT : DEV_PAGE_RANGE);
   }
+  if ((int64_t)wb * share >= total) return;  // a block without work
   __syncthreads();
-  // warp k joins the item that begins in it; the last warp also the one that comes in
-  const int wb = blockIdx.x * pl.warps, we = wb + pl.warps - 1;  // the block's workers
-  auto place = [&](const Split& sp, int& w0, int& w1, int& h, int& rows) {
-    w0 = (int)paged_div(sp.start, share);
-    w1 = (int)paged_div(sp.start + sp.tiles - 1, share);
-    const int hk = sp.item / pl.qtiles, q0 = (sp.item - hk * pl.qtiles) * QR;
-    h = hk * pl.group + q0;
-    rows = min(QR, pl.group - q0);
-  };
-  for (int k = warp == pl.warps - 1 ? 0 : warp + 1; k <= warp + 1; k += warp + 1) {
+  // a thread joins four elements of a split item's row over the block's pieces
+  constexpr int VEC = HD / 4;
+  const int cols = pl.rows * VEC, bytes = S::warp_bytes(pl.rows), tail = S::head(pl.rows);
+  for (int i = threadIdx.x; i < (pl.warps + 1) * cols; i += blockDim.x) {
+    const int k = i / cols, col = i - k * cols, row = col / VEC, v = col - row * VEC;
     const Split sp = s_split[k];
-    if (sp.seq < 0) continue;
-    int w0, w1, h, rows;
-    place(sp, w0, w1, h, rows);
-    const bool inside = k > 0 && w1 <= we;
-    T* out = static_cast<T*>(a.out) + sp.seq * a.ldo + h * HD;
-    float* lse = a.lse ? a.lse + (int64_t)sp.seq * a.nh + h : nullptr;
-    const int64_t slot = ((int64_t)blockIdx.x * 2 + (k > 0 ? 1 : 0)) * pl.rows;
-    const int p0 = max(w0, wb) - wb, p1 = min(w1, we) - wb;  // the warps with a piece
-    constexpr int VEC = HD / 4;
-    for (int col = lane; col < rows * VEC; col += 32) {
-      const int row = col / VEC, v = col - row * VEC;
-      PatSum sum;
-      for (int p = p0; p <= p1; ++p) {
-        const char* piece = pat_smem + p * S::warp_bytes(pl.rows) + (k > 0 && p == p0 ? 0 : S::head(pl.rows));
-        sum.add(reinterpret_cast<const float2*>(piece + pl.rows * HD * 4)[row], reinterpret_cast<const float4*>(piece)[col]);
+    if (sp.seq < 0 || row >= sp.rows) continue;
+    const int p0 = max(sp.w0, wb) - wb, p1 = min(sp.w1, we) - wb;  // the warps with a piece
+    PatSum sum;
+    for (int p = p0; p <= p1; p += 4) {
+      float2 ml[4];
+      float4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.f);
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p + j <= p1) {  // all pieces but the one that begins the item are head pieces
+          const char* piece = pat_smem + (p + j) * bytes + (k > 0 && p + j == p0 ? 0 : tail);
+          ml[j] = reinterpret_cast<const float2*>(piece + pl.rows * HD * 4)[row];
+          x[j] = reinterpret_cast<const float4*>(piece)[col];
+        }
       }
-      if (inside) {
-        sum.store(out + col * 4, lse && v == 0 ? lse + row : nullptr);
-      } else {
-        reinterpret_cast<float4*>(pl.part + slot * HD)[col] = sum.o;
-        if (v == 0) pl.ml[slot + row] = make_float2(sum.m, sum.l);
-      }
+      sum.add(ml, x);
     }
-    if (!inside) {
-      __syncwarp();
-      if (lane == 0) s_last[k > 0] = pat_arrive(pl.arrived + w0 / pl.warps, pl.tag, w1 / pl.warps - w0 / pl.warps + 1);
+    if (k > 0 && sp.w1 <= we) {
+      sum.store(static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD + col * 4,
+                a.lse && v == 0 ? a.lse + (int64_t)sp.seq * a.nh + sp.h + row : nullptr);
+    } else {
+      const int64_t slot = ((int64_t)blockIdx.x * 2 + (k > 0 ? 1 : 0)) * pl.rows;
+      reinterpret_cast<float4*>(pl.part + slot * HD)[col] = sum.o;
+      if (v == 0) pl.ml[slot + row] = make_float2(sum.m, sum.l);
     }
   }
+  if (s_cross[0] < 0 && s_cross[1] < 0) return;
   __syncthreads();
-  for (int i = 0; i < 2; ++i) {
-    if (!s_last[i]) continue;
-    int k = 0;  // the item that goes on begins in the last worker with a tail piece
-    if (i == 1)
-      for (k = pl.warps; s_split[k].seq < 0;) --k;
-    const Split sp = s_split[k];
-    int w0, w1, h, rows;
-    place(sp, w0, w1, h, rows);
-    pat_join<T, HD>(pl, w0 / pl.warps, w1 / pl.warps, rows, static_cast<T*>(a.out) + sp.seq * a.ldo + h * HD,
-                    a.lse ? a.lse + (int64_t)sp.seq * a.nh + h : nullptr, pat_smem);
-  }
+  for (int i = 0; i < 2; ++i)
+    if (warp == (i == 0 ? 0 : pl.warps - 1) && s_cross[i] >= 0) {
+      const Split sp = s_split[s_cross[i]];
+      const bool last = pat_arrive(pl.flags, pl.tag, sp.w0 / pl.warps, sp.w1 / pl.warps);
+      if (lane == 0) s_last[i] = last;
+    }
+  __syncthreads();
+  if (!s_last[0] && !s_last[1]) return;
+  // two items: half of the threads each
+  const bool both = s_last[0] && s_last[1];
+  const int threads = both ? blockDim.x / 2 : blockDim.x;
+  const int i = both ? (int)threadIdx.x >= threads : !s_last[0];
+  const Split sp = s_split[s_cross[i]];
+  pat_join<T, HD>(pl, sp.w0 / pl.warps, sp.w1 / pl.warps, sp.rows, static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD,
+                  a.lse ? a.lse + (int64_t)sp.seq * a.nh + sp.h : nullptr, pat_smem, threadIdx.x - (both ? i * threads : 0),
+                  threads, (cols + threads - 1) / threads);
 }
 
 }  // namespace g2
