@@ -1212,7 +1212,10 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedApp
   const bool bf = kv->dtype == GPT2_BF16;
   auto kern = bf ? (pairs ? paged_append_kernel<bf16, true> : paged_append_kernel<bf16, false>)
                  : (pairs ? paged_append_kernel<float, true> : paged_append_kernel<float, false>);
-  kern<<<grid, PKV_THREADS, 0, c.stream>>>(a);
+  LaunchCtx cp = c;
+  cp.pdl = true;
+  const cudaError_t e = launch_k(cp, kern, grid, dim3(PKV_THREADS), 0, a);
+  if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_kv_append: ") + cudaGetErrorString(e));
   return check_launch(c, "paged_kv_append");
 }
 
@@ -1289,7 +1292,9 @@ int paged_attention_inst(const LaunchCtx& c, const gpt2_paged_kv* kv, const Page
   pl.ml = reinterpret_cast<float2*>(p);
   p += (size_t)grid * 2 * pl.rows * 8;
   pl.flags = reinterpret_cast<unsigned long long*>(p);
-  const cudaError_t e = launch_k(c, paged_attn_kernel<T, HD, QR, BOX>, dim3(grid), dim3(pl.warps * 32),
+  LaunchCtx cp = c;
+  cp.pdl = true;
+  const cudaError_t e = launch_k(cp, paged_attn_kernel<T, HD, QR, BOX>, dim3(grid), dim3(pl.warps * 32),
                                  S::smem(pl.rows, a.c.n_seqs), a, pl, km, vm);
   if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_attention: ") + cudaGetErrorString(e));
   return check_launch(c, "paged_attention");

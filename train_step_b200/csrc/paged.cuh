@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(PKV_THREADS) paged_append_kernel(const PagedAp
   constexpr int VN = 16 / sizeof(T);
   __shared__ int64_t s_off[PKV_MAX_ROWS];  // element offset of the slot, -1: skip the row
   __shared__ int s_pos[PKV_MAX_ROWS];
+  pdl_launch_dependents();
+  pdl_wait();
   const int row0 = blockIdx.x * a.rows_per_block;
   const int nrows = min(a.rows_per_block, a.rows - row0);
   if ((int)threadIdx.x < nrows) {
@@ -265,23 +267,35 @@ struct PagedAttnPlan {
 // the flags may hold anything before a call; they are clear after it, so that a captured call
 // may run again with the same tag. No block waits for another, and no atomic is contended (a
 // counter with compare-and-swap took a microsecond per block that arrived at the same time).
-// One warp calls this, after a barrier behind the block's writes.
-__device__ __forceinline__ bool pat_arrive(unsigned long long* flags, unsigned long long tag, int b0, int b1) {
+// One warp calls this for the item that comes in from the block before (0) and the one that goes
+// on in the next (1), of blocks b0[i]..b1[i] (b0[i] < 0: none), after a barrier behind the block's
+// writes; last[i]: the block joins item i.
+__device__ __forceinline__ void pat_arrive(unsigned long long* flags, unsigned long long tag, const int (&b0)[2],
+                                           const int (&b1)[2], bool (&last)[2]) {
   const int lane = threadIdx.x & 31;
-  // a block's flag of the item that begins in it is its second
   if (lane == 0) {
     __threadfence();
-    *reinterpret_cast<volatile unsigned long long*>(flags + 2 * blockIdx.x + ((int)blockIdx.x == b0)) = tag;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)  // a block's flag of the item that begins in it is its second
+      if (b0[i] >= 0) *reinterpret_cast<volatile unsigned long long*>(flags + 2 * blockIdx.x + i) = tag;
+    asm volatile("fence.sc.gpu;" ::: "memory");
   }
   __syncwarp();
-  asm volatile("fence.sc.gpu;" ::: "memory");
-  bool all = true;
-  for (int b = b0 + lane; b <= b1; b += 32)
-    all &= *reinterpret_cast<volatile unsigned long long*>(flags + 2 * b + (b == b0)) == tag;
-  if (!__all_sync(0xffffffffu, all)) return false;
-  __threadfence();
-  for (int b = b0 + lane; b <= b1; b += 32) flags[2 * b + (b == b0)] = 0ull;
-  return true;
+  bool all[2] = {b0[0] >= 0, b0[1] >= 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (b0[i] >= 0)
+      for (int b = b0[i] + lane; b <= b1[i]; b += 32) {
+        unsigned long long f;
+        asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(f) : "l"(flags + 2 * b + (b == b0[i])) : "memory");
+        all[i] &= f == tag;
+      }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    last[i] = __all_sync(0xffffffffu, all[i]);
+    if (last[i])
+      for (int b = b0[i] + lane; b <= b1[i]; b += 32) flags[2 * b + (b == b0[i])] = 0ull;
+  }
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
@@ -749,8 +763,8 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   // items that are split, for the joins: [0] the one that begins before the block's first
   // worker, [1 + warp] the one that begins in a warp and does not end there (seq < 0: none)
   struct Split {
-    int seq, w0, w1;  // its workers, over all blocks
-    int h, rows;      // its query heads
+    int seq, h, rows;    // its query heads
+    int b0, b1, p0, p1;  // its blocks, and the warps of this block that have a piece of it
   };
   __shared__ Split s_split[S::MAX_WARPS + 1];
   __shared__ int s_cross[2];  // which of them other blocks share: the one that comes in, that goes on (-1: none)
@@ -780,6 +794,8 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       s_last[0] = s_last[1] = s_no_abort = 0;
     }
   }
+  pdl_launch_dependents();
+  pdl_wait();  // nothing above touches global memory
   pat_prefix(a, before);
   const int B = a.c.n_seqs;
   // sequences without tokens
@@ -937,7 +953,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
           const int64_t start = u0 + t - c.tile;  // the item's first tile
           const int k = from == 0 ? warp + 1 : 0, w0 = from == 0 ? w : (int)paged_div(start, share);
           const int w1 = (int)paged_div(start + c.tiles - 1, share);
-          s_split[k] = Split{c.seq, w0, w1, h, out.rows};
+          s_split[k] = Split{c.seq, h, out.rows, w0 / pl.warps, w1 / pl.warps, max(w0 - wb, 0), min(w1, we) - wb};
           if (k == 0 || w1 > we) s_cross[k > 0] = k;
         }
       }
@@ -959,24 +975,23 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
     const int k = i / cols, col = i - k * cols, row = col / VEC, v = col - row * VEC;
     const Split sp = s_split[k];
     if (sp.seq < 0 || row >= sp.rows) continue;
-    const int p0 = max(sp.w0, wb) - wb, p1 = min(sp.w1, we) - wb;  // the warps with a piece
     PatSum sum;
-    for (int p = p0; p <= p1; p += 4) {
+    for (int p = sp.p0; p <= sp.p1; p += 4) {
       float2 ml[4];
       float4 x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         ml[j] = make_float2(-INFINITY, 0.f);
         x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p + j <= p1) {  // all pieces but the one that begins the item are head pieces
-          const char* piece = pat_smem + (p + j) * bytes + (k > 0 && p + j == p0 ? 0 : tail);
+        if (p + j <= sp.p1) {  // all pieces but the one that begins the item are head pieces
+          const char* piece = pat_smem + (p + j) * bytes + (k > 0 && p + j == sp.p0 ? 0 : tail);
           ml[j] = reinterpret_cast<const float2*>(piece + pl.rows * HD * 4)[row];
           x[j] = reinterpret_cast<const float4*>(piece)[col];
         }
       }
       sum.add(ml, x);
     }
-    if (k > 0 && sp.w1 <= we) {
+    if (k > 0 && sp.b1 == (int)blockIdx.x) {
       sum.store(static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD + col * 4,
                 a.lse && v == 0 ? a.lse + (int64_t)sp.seq * a.nh + sp.h + row : nullptr);
     } else {
@@ -987,12 +1002,22 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   }
   if (s_cross[0] < 0 && s_cross[1] < 0) return;
   __syncthreads();
-  for (int i = 0; i < 2; ++i)
-    if (warp == (i == 0 ? 0 : pl.warps - 1) && s_cross[i] >= 0) {
-      const Split sp = s_split[s_cross[i]];
-      const bool last = pat_arrive(pl.flags, pl.tag, sp.w0 / pl.warps, sp.w1 / pl.warps);
-      if (lane == 0) s_last[i] = last;
+  if (warp == 0) {
+    int b0[2], b1[2];
+    bool last[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      b0[i] = b1[i] = -1;
+      if (s_cross[i] < 0) continue;
+      b0[i] = s_split[s_cross[i]].b0;
+      b1[i] = s_split[s_cross[i]].b1;
     }
+    pat_arrive(pl.flags, pl.tag, b0, b1, last);
+    if (lane == 0) {
+      s_last[0] = last[0];
+      s_last[1] = last[1];
+    }
+  }
   __syncthreads();
   if (!s_last[0] && !s_last[1]) return;
   // two items: half of the threads each
@@ -1000,7 +1025,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   const int threads = both ? blockDim.x / 2 : blockDim.x;
   const int i = both ? (int)threadIdx.x >= threads : !s_last[0];
   const Split sp = s_split[s_cross[i]];
-  pat_join<T, HD>(pl, sp.w0 / pl.warps, sp.w1 / pl.warps, sp.rows, static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD,
+  pat_join<T, HD>(pl, sp.b0, sp.b1, sp.rows, static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD,
                   a.lse ? a.lse + (int64_t)sp.seq * a.nh + sp.h : nullptr, pat_smem, threadIdx.x - (both ? i * threads : 0),
                   threads, (cols + threads - 1) / threads);
 }
