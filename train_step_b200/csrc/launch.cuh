@@ -1269,18 +1269,16 @@ inline bool encode_paged_map(CUtensorMap* map, const void* ptr, const gpt2_paged
 template <class T, int HD, int QR, bool BOX>
 int paged_attention_inst(const LaunchCtx& c, const gpt2_paged_kv* kv, const PagedAttnArgs& a, void* ws) {
   using S = PatShape<T, HD, QR>;
-  constexpr int SMEM_MAX = 226 * 1024;
-  static_assert(S::warps(QR) >= 1 && S::smem(QR, PAGED_MAX_SEQS) <= SMEM_MAX && S::smem(1, PAGED_MAX_SEQS) <= SMEM_MAX,
-                "rings too large");
+  static_assert(S::warps(QR, PAGED_MAX_SEQS) >= 1, "rings too large");
   CUtensorMap km{}, vm{};
   if (BOX && (!encode_paged_map(&km, kv->k, kv) || !encode_paged_map(&vm, kv->v, kv)))
     return paged_attention_inst<T, HD, QR, false>(c, kv, a, ws);
-  if (!smem_optin(paged_attn_kernel<T, HD, QR, BOX>, SMEM_MAX))
+  if (!smem_optin(paged_attn_kernel<T, HD, QR, BOX>, PAT_SMEM))
     return fail(c, GPT2_ERR_CUDA, "paged_attention: shared memory opt-in failed");
   PagedAttnPlan pl;
   pl.group = a.nh / a.c.nkv;
   pl.rows = std::min(QR, pl.group);
-  pl.warps = S::warps(pl.rows);
+  pl.warps = S::warps(pl.rows, a.c.n_seqs);
   const int grid = std::min(c.num_sms, PAT_MAX_BLOCKS);
   pl.workers = grid * pl.warps;
   pl.qtiles = (pl.group + QR - 1) / QR;

@@ -212,7 +212,7 @@ struct PagedAttnArgs {
 // warps per scheduler, each a chain of dependent steps): 16-byte copies by all lanes took half
 // of a tile's instructions, which is what the tensor copies save.
 constexpr int PAT_MAX_BLOCKS = 256;
-constexpr int PAT_SMEM = 204 * 1024;  // of the workers of a block
+constexpr int PAT_SMEM = 226 * 1024;  // of a block
 
 template <class T, int HD, int QR_>
 struct PatShape {
@@ -224,8 +224,7 @@ struct PatShape {
   static constexpr int BOXES = (ROW + BOX_ROW - 1) / BOX_ROW;
   static constexpr int BOX = PAT_TILE * BOX_ROW;
   static constexpr int TILE = BOXES * BOX;
-  static constexpr int STAGES = 2;
-  static constexpr int MAX_WARPS = 12;
+  static constexpr int STAGES = 2;  // more of them cost warps, and were slower
   // fp32: a copy of the item's queries and the tile's weights, per warp
   static constexpr int SIDE = sizeof(T) == 4 ? QR * ROW + QR * PAT_TILE * 4 : 0;
   // a piece: outputs, then (maximum, sum), of each row; a warp: its ring of keys and values
@@ -237,11 +236,18 @@ struct PatShape {
   __host__ __device__ static constexpr int warp_bytes(int rows) {
     return (head(rows) + piece(rows) + SIDE + STAGES * 12 + 1023) / 1024 * 1024;
   }
-  static constexpr int warps(int rows) {
-    return PAT_SMEM / warp_bytes(rows) > MAX_WARPS ? MAX_WARPS : PAT_SMEM / warp_bytes(rows);
+  // workers of a block: as many as fit beside the n_seqs + 1 counts (the first 1024 bytes align
+  // the rest)
+  static constexpr int warps(int rows, int n_seqs) {
+    const int fit = (PAT_SMEM - 1024 - (n_seqs + 1) * 4) / warp_bytes(rows);
+    return fit > 12 ? 12 : fit;
   }
-  // the first 1024 bytes align the rest
-  static constexpr int smem(int rows, int n_seqs) { return 1024 + warps(rows) * warp_bytes(rows) + (n_seqs + 1) * 4; }
+  static constexpr int smem(int rows, int n_seqs) {
+    return 1024 + warps(rows, n_seqs) * warp_bytes(rows) + (n_seqs + 1) * 4;
+  }
+  // the smallest group that comes to this shape
+  static constexpr int MIN_ROWS = sizeof(T) == 2 ? (QR == 16 ? 9 : 1) : QR == 8 ? 5 : QR == 4 ? 2 : 1;
+  static constexpr int MAX_WARPS = warps(MIN_ROWS, 1);
 
   // 16-byte chunk `c` of row `r` in a tile: the order in which a tensor copy with 128-byte (64-byte
   // for 64-byte rows) swizzling leaves it; consecutive rows of a chunk are in different banks
