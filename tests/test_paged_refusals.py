@@ -148,6 +148,14 @@ int main() {
   bad = 0;
   if (paged_length(-3, 10, &bad) != 0 || !bad) return 7;
 
+  for (int d : {1, 2, 3, 7, 48, 144, 1000, 65537, 0x7fffffff})
+    for (int64_t x : {0LL, 1LL, 2LL, 143LL, 144LL, 1LL << 20, 0x7ffffffeLL, 0x7fffffffLL})
+      for (int64_t k : {-1LL, 0LL, 1LL}) {
+        const int64_t y = x / d * d + k;  // around every multiple
+        if (y >= 0 && y <= 0x7fffffff && paged_div_by((int)y, d, 0xffffffffu / d) != y / d) return 14;
+        if (paged_div_by((int)x, d, 0xffffffffu / d) != x / d) return 15;
+      }
+
   // every worker's walk over its share, one after the other, is the whole order
   srand(1);
   for (int trial = 0; trial < 3000; ++trial) {

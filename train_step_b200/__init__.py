@@ -654,15 +654,14 @@ class PagedKV:
     def _rows(self, name, t, rows, heads):
         """[rows, heads, head_dim] of the cache's type and device, heads contiguous: the row stride."""
         st = t.stride()
-        if (tuple(t.shape) != (rows, heads, self.head_dim) or t.dtype is not self.dtype
+        if (t.shape != (rows, heads, self.head_dim) or t.dtype is not self.dtype
                 or t.get_device() != self._index or st[2] != 1 or (st[1] != self.head_dim and heads > 1)):
             raise ValueError(f"{name} must be [{rows}, {heads}, {self.head_dim}] {self.dtype} on {self.device}, "
                              "with the heads of a row contiguous")
         return st[0] if rows > 1 else heads * self.head_dim
 
     def _ints(self, name, t, n):
-        if (t.dtype is not self._int32 or tuple(t.shape) != (n,) or t.get_device() != self._index
-                or (t.stride(0) != 1 and n > 1)):
+        if (t.dtype is not self._int32 or t.shape != (n,) or t.get_device() != self._index or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {self.device}")
         return t.data_ptr()
 
@@ -720,7 +719,7 @@ def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None
     lens = cache._ints("seq_lens", seq_lens, B)
     pl = None
     if lse is not None:
-        if (lse.dtype is not cache._float32 or tuple(lse.shape) != (B, nh) or lse.get_device() != cache._index
+        if (lse.dtype is not cache._float32 or lse.shape != (B, nh) or lse.get_device() != cache._index
                 or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous fp32 tensor [{B}, {nh}] on {cache.device}")
         pl = lse.data_ptr()

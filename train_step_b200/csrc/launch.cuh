@@ -1202,21 +1202,25 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedApp
   if (a.rot && (!a.cos_sin || a.n_positions < 1 || (reinterpret_cast<uintptr_t>(a.cos_sin) & 15)))
     return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: a rotation needs a 16-byte aligned cos_sin table");
   a.tasks_per_row = (a.nh + 2 * a.c.nkv) * (hd / (2 * vn));
-  // four tasks per thread, in rows of at most PKV_MAX_ROWS per block, as long as that leaves
-  // two blocks per SM; otherwise fewer rows and a row's tasks over several blocks
-  a.rows_per_block = std::max(1, std::min(PKV_MAX_ROWS, 4 * PKV_THREADS / a.tasks_per_row));
-  while (a.rows_per_block > 1 && (a.rows + a.rows_per_block - 1) / a.rows_per_block < 2 * c.num_sms)
-    a.rows_per_block /= 2;
-  const dim3 grid((a.rows + a.rows_per_block - 1) / a.rows_per_block,
-                  std::max(1, (a.rows_per_block * a.tasks_per_row + 4 * PKV_THREADS - 1) / (4 * PKV_THREADS)));
+  a.per_row = 0xffffffffu / a.tasks_per_row;
+  a.per_head = 0xffffffffu / (hd / (2 * vn));
   const bool bf = kv->dtype == GPT2_BF16;
   auto kern = bf ? (pairs ? paged_append_kernel<bf16, true> : paged_append_kernel<bf16, false>)
                  : (pairs ? paged_append_kernel<float, true> : paged_append_kernel<float, false>);
   LaunchCtx cp = c;
   cp.pdl = true;
-  const cudaError_t e = launch_k(cp, kern, grid, dim3(PKV_THREADS), 0, a);
-  if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_kv_append: ") + cudaGetErrorString(e));
-  return check_launch(c, "paged_kv_append");
+  // one launch for up to 2^30 tasks; a grid that fills every SM
+  const int most = (1 << 30) / a.tasks_per_row;
+  const int rows = a.rows;
+  for (int row0 = 0; row0 < rows; row0 += most) {
+    a.row0 = row0;
+    a.tasks = std::min(rows - row0, most) * a.tasks_per_row;
+    const int grid = std::min((a.tasks + PKV_THREADS - 1) / PKV_THREADS, PKV_BLOCKS * c.num_sms);
+    const cudaError_t e = launch_k(cp, kern, dim3(grid), dim3(PKV_THREADS), 0, a);
+    if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_kv_append: ") + cudaGetErrorString(e));
+    if ((r = check_launch(c, "paged_kv_append"))) return r;
+  }
+  return GPT2_OK;
 }
 
 inline bool paged_heads_ok(int nh, int nkv) { return nkv >= 1 && nh >= 1 && nh <= 4096 && nh % nkv == 0; }

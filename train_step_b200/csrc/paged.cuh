@@ -34,7 +34,7 @@ __device__ __forceinline__ int paged_page(const PagedView& c, int seq, int pos) 
 // append
 // ---------------------------------------------------------------------------
 constexpr int PKV_THREADS = 256;
-constexpr int PKV_MAX_ROWS = 32;  // rows of one block
+constexpr int PKV_BLOCKS = 8;  // per SM
 
 struct PagedAppendArgs {
   PagedView c;
@@ -47,7 +47,9 @@ struct PagedAppendArgs {
   const int* seqs;  // nullable: row n belongs to sequence n
   const float* cos_sin;
   int n_positions, rot;
-  int rows_per_block, tasks_per_row;
+  int64_t row0;  // of this launch
+  int tasks, tasks_per_row;
+  uint32_t per_row, per_head;  // inverses of the tasks of a row and of a head, for paged_div_by
 };
 
 __device__ __forceinline__ void pkv_unpack(const uint4& r, float (&f)[8], bf16) {
@@ -73,73 +75,63 @@ __device__ __forceinline__ uint4 pkv_pack(const float (&f)[4], float) {
 // nothing.
 // A task is two 16-byte vectors that hold both elements of their pairs (for rotated halves
 // vectors rot/2 apart, otherwise neighbours), so every element is read and written once and
-// q_out may be q. Bound by HBM: the row is read and written once.
+// q_out may be q. Bound by HBM: the row is read and written once. A thread reads its vectors
+// before it looks up where they go (position, then page, then the table row): the two latencies
+// overlap. The grid fills every SM once (a grid of many short blocks spent a fifth of the time
+// on starting them), so 32 registers a thread are allowed. 16,384 rows of 12 + 12 + 12 heads of
+// 64 in bf16, 151 MB moved: 27.8 us, 5.4 TB/s (a plain copy of as many bytes: 24.6 us).
 template <class T, bool PAIRS>
-__global__ void __launch_bounds__(PKV_THREADS) paged_append_kernel(const PagedAppendArgs a) {
+__global__ void __launch_bounds__(PKV_THREADS, PKV_BLOCKS) paged_append_kernel(const PagedAppendArgs a) {
   constexpr int VN = 16 / sizeof(T);
-  __shared__ int64_t s_off[PKV_MAX_ROWS];  // element offset of the slot, -1: skip the row
-  __shared__ int s_pos[PKV_MAX_ROWS];
   pdl_launch_dependents();
   pdl_wait();
-  const int row0 = blockIdx.x * a.rows_per_block;
-  const int nrows = min(a.rows_per_block, a.rows - row0);
-  if ((int)threadIdx.x < nrows) {
-    const int n = row0 + threadIdx.x;
-    const int pos = a.positions[n];
-    int64_t off = -1;
-    if (pos >= 0) {
-      const int seq = a.seqs ? a.seqs[n] : n;
-      int page = -1;
-      if ((unsigned)seq < (unsigned)a.c.n_seqs && (pos >> a.c.log2_page) < a.c.max_pages &&
-          (a.rot == 0 || pos < a.n_positions))
-        page = paged_page(a.c, seq, pos);
-      if (page >= 0)
-        off = page * a.c.page_stride + (pos & ((1 << a.c.log2_page) - 1)) * a.c.row_stride;
-      else
-        raise_device_error(a.c.status, DEV_PAGE_RANGE);
-    }
-    s_off[threadIdx.x] = off;
-    s_pos[threadIdx.x] = pos;
-  }
-  __syncthreads();
-  const int hp = a.c.hd / (2 * VN);      // tasks per head
-  const int nrot = a.rot / (2 * VN);     // of which rotated
-  const int total = nrows * a.tasks_per_row;
-  for (int i = blockIdx.y * PKV_THREADS + threadIdx.x; i < total; i += gridDim.y * PKV_THREADS) {
-    const int r = i / a.tasks_per_row, t = i - r * a.tasks_per_row;
-    const int64_t off = s_off[r];
-    if (off < 0) continue;
-    const int hh = t / hp, j = t - hh * hp;
-    const int64_t n = row0 + r;
+  const int hp = a.c.hd / (2 * VN);   // tasks per head
+  const int nrot = a.rot / (2 * VN);  // of which rotated
+  const int step = gridDim.x * PKV_THREADS;
+  for (int i = blockIdx.x * PKV_THREADS + threadIdx.x; i < a.tasks; i += step) {
+    const int r = paged_div_by(i, a.tasks_per_row, a.per_row), t = i - r * a.tasks_per_row;
+    const int64_t n = a.row0 + r;
+    int hh = paged_div_by(t, hp, a.per_head);
+    const int j = t - hh * hp;
+    // values are cut into the same pieces as keys
+    const bool halves = !PAIRS && j < nrot;
+    const int at = halves ? j * VN : j * 2 * VN, gap = halves ? a.rot / 2 : VN;
     const T* src;
     T* dst;
-    bool turn = j < nrot;
+    int64_t head = 0;
+    bool turn = j < nrot, cached = true;
     if (hh < a.nh) {
       src = static_cast<const T*>(a.q) + n * a.ldq + hh * a.c.hd;
       dst = static_cast<T*>(a.q_out) + n * a.ldqo + hh * a.c.hd;
-    } else if (hh < a.nh + a.c.nkv) {
-      const int h = hh - a.nh;
-      src = static_cast<const T*>(a.k) + n * a.ldk + h * a.c.hd;
-      dst = static_cast<T*>(a.c.k) + off + h * a.c.head_stride;
+      cached = false;
+    } else if ((hh -= a.nh) < a.c.nkv) {
+      src = static_cast<const T*>(a.k) + n * a.ldk + hh * a.c.hd;
+      dst = static_cast<T*>(a.c.k);
+      head = hh * a.c.head_stride;
     } else {
-      const int h = hh - a.nh - a.c.nkv;
-      src = static_cast<const T*>(a.v) + n * a.ldv + h * a.c.hd;
-      dst = static_cast<T*>(a.c.v) + off + h * a.c.head_stride;
+      hh -= a.c.nkv;
+      src = static_cast<const T*>(a.v) + n * a.ldv + hh * a.c.hd;
+      dst = static_cast<T*>(a.c.v);
+      head = hh * a.c.head_stride;
       turn = false;
     }
-    int ia = j * 2 * VN, ib = ia + VN;
-    if (turn && !PAIRS) {
-      ia = j * VN;
-      ib = a.rot / 2 + ia;
-    } else if (!PAIRS && j < nrot) {
-      ia = j * VN;  // a value head: the same pieces, copied
-      ib = a.rot / 2 + ia;
+    uint4 va = *reinterpret_cast<const uint4*>(src + at);
+    uint4 vb = *reinterpret_cast<const uint4*>(src + at + gap);
+    const int pos = a.positions[n];
+    if (pos < 0) continue;
+    const int seq = a.seqs ? a.seqs[n] : (int)n;
+    int page = -1;
+    if ((unsigned)seq < (unsigned)a.c.n_seqs && (pos >> a.c.log2_page) < a.c.max_pages &&
+        (a.rot == 0 || pos < a.n_positions))
+      page = paged_page(a.c, seq, pos);
+    if (page < 0) {
+      raise_device_error(a.c.status, DEV_PAGE_RANGE);
+      continue;
     }
-    uint4 va = *reinterpret_cast<const uint4*>(src + ia);
-    uint4 vb = *reinterpret_cast<const uint4*>(src + ib);
+    if (cached) dst += page * a.c.page_stride + (pos & ((1 << a.c.log2_page) - 1)) * a.c.row_stride + head;
     if (turn) {
       // VN cosines and VN sines, for the pairs j * VN ...
-      const float* cs = a.cos_sin + (int64_t)s_pos[r] * a.rot + j * VN;
+      const float* cs = a.cos_sin + (int64_t)pos * a.rot + j * VN;
       float c[VN], s[VN];
 #pragma unroll
       for (int e = 0; e < VN; e += 4) {
@@ -171,8 +163,8 @@ __global__ void __launch_bounds__(PKV_THREADS) paged_append_kernel(const PagedAp
       va = pkv_pack(x, T());
       vb = pkv_pack(y, T());
     }
-    *reinterpret_cast<uint4*>(dst + ia) = va;
-    *reinterpret_cast<uint4*>(dst + ib) = vb;
+    *reinterpret_cast<uint4*>(dst + at) = va;
+    *reinterpret_cast<uint4*>(dst + at + gap) = vb;
   }
 }
 

@@ -62,6 +62,11 @@ G2_HD int paged_length(int len, int capacity, int* bad) {
 G2_HD int64_t paged_div(int64_t x, int64_t d) {  // 0 <= x, 1 <= d; nearly always 32-bit numbers
   return ((x | d) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
 }
+// x / d for 0 <= x < 2^31 with inverse = (2^32 - 1) / d: the high product is at most one too small.
+G2_HD int paged_div_by(int x, int d, uint32_t inverse) {
+  const int q = (int)(((uint64_t)(uint32_t)x * inverse) >> 32);
+  return q + (x - q * d >= d);
+}
 G2_HD int64_t paged_share(int64_t total, int workers) {
   const int64_t s = paged_div(total + workers - 1, workers);
   return s < 1 ? 1 : s;
