@@ -75,7 +75,7 @@ def test_a_null_cache_is_refused():
     (dict(ldv=132), CONFIG), (dict(q=None), CONFIG), (dict(q_out=None), CONFIG), (dict(nh=0), CONFIG),
     (dict(nh=-1), CONFIG), (dict(nh=5000, ldq=320000, ldqo=320000), CONFIG), (dict(ldq=248), CONFIG),
     (dict(ldqo=260), CONFIG), (dict(q_out=A + 4), CONFIG), (dict(N=-1), CONFIG), (dict(positions=None), CONFIG),
-    (dict(seqs=None, N=4), BATCH), (dict(rot=8), CONFIG), (dict(rot=80), CONFIG), (dict(rot=-16), CONFIG),
+    (dict(seqs=None, N=4), BATCH), (dict(N=1 << 29), BATCH), (dict(rot=8), CONFIG), (dict(rot=80), CONFIG), (dict(rot=-16), CONFIG),
     (dict(cos_sin=None), CONFIG), (dict(cos_sin=A + 4), CONFIG), (dict(n_positions=0), CONFIG),
 ])
 def test_append_refuses(change, code):
@@ -162,14 +162,16 @@ int main() {
     const int n_seqs = 1 + rand() % 9, items = 1 + rand() % 5, workers = 1 + rand() % 40;
     std::vector<int> before(n_seqs + 1, 0);
     for (int b = 0; b < n_seqs; ++b) before[b + 1] = before[b] + (rand() % 3 ? rand() % 14 : 0);
-    const int64_t total = (int64_t)before[n_seqs] * items, share = paged_share(total, workers);
+    const int64_t total = (int64_t)before[n_seqs] * items, share = paged_share(total, workers, 0xffffffffu / workers);
     if (share < 1 || share * workers < total) return 8;
     int64_t u = 0;
     int seq = -1, item = items - 1, tile = 0, tiles = 1;  // the walk that is expected
     for (int w = 0; w < workers; ++w) {
       const int64_t a = w * share, e = a + share < total ? a + share : total;
       if (a >= e) continue;
-      PagedCursor c = paged_locate(before.data(), n_seqs, items, a);
+      int at = 0;  // the sequence of tile a
+      while ((int64_t)before[at + 1] * items <= a) ++at;
+      PagedCursor c = paged_place(before.data(), at, items, a);
       for (int64_t i = a; i < e; ++i, ++u) {
         if (i > a) {
           const int was = c.seq;

@@ -1202,6 +1202,9 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedApp
   if (a.rot && (!a.cos_sin || a.n_positions < 1 || (reinterpret_cast<uintptr_t>(a.cos_sin) & 15)))
     return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: a rotation needs a 16-byte aligned cos_sin table");
   a.tasks_per_row = (a.nh + 2 * a.c.nkv) * (hd / (2 * vn));
+  if ((int64_t)a.rows * a.tasks_per_row > (1 << 30))
+    return fail(c, GPT2_ERR_BATCH, "paged_kv_append: more than 2^30 pairs of 16-byte vectors");
+  a.tasks = a.rows * a.tasks_per_row;
   a.per_row = 0xffffffffu / a.tasks_per_row;
   a.per_head = 0xffffffffu / (hd / (2 * vn));
   const bool bf = kv->dtype == GPT2_BF16;
@@ -1209,32 +1212,25 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedApp
                  : (pairs ? paged_append_kernel<float, true> : paged_append_kernel<float, false>);
   LaunchCtx cp = c;
   cp.pdl = true;
-  // one launch for up to 2^30 tasks; a grid that fills every SM
-  const int most = (1 << 30) / a.tasks_per_row;
-  const int rows = a.rows;
-  for (int row0 = 0; row0 < rows; row0 += most) {
-    a.row0 = row0;
-    a.tasks = std::min(rows - row0, most) * a.tasks_per_row;
-    const int grid = std::min((a.tasks + PKV_THREADS - 1) / PKV_THREADS, PKV_BLOCKS * c.num_sms);
-    const cudaError_t e = launch_k(cp, kern, dim3(grid), dim3(PKV_THREADS), 0, a);
-    if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_kv_append: ") + cudaGetErrorString(e));
-    if ((r = check_launch(c, "paged_kv_append"))) return r;
-  }
-  return GPT2_OK;
+  // a grid that fills every SM
+  const int grid = std::min((a.tasks + PKV_THREADS - 1) / PKV_THREADS, PKV_BLOCKS * c.num_sms);
+  const cudaError_t e = launch_k(cp, kern, dim3(grid), dim3(PKV_THREADS), 0, a);
+  if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_kv_append: ") + cudaGetErrorString(e));
+  return check_launch(c, "paged_kv_append");
 }
 
 inline bool paged_heads_ok(int nh, int nkv) { return nkv >= 1 && nh >= 1 && nh <= 4096 && nh % nkv == 0; }
 
-// Partial results of at most PAT_MAX_BLOCKS blocks: two each, of min(16, group) rows, with a
-// flag.
+// Partial results of at most PAT_MAX_BLOCKS blocks: two each, of min(16, group) rows; and an
+// arrival word each.
 inline size_t paged_attention_ws_bytes(int n_seqs, int nh, int nkv, int hd) {
   if (n_seqs < 0 || n_seqs > PAGED_MAX_SEQS || !paged_heads_ok(nh, nkv) || hd < 1 || hd > 128) return 0;
   const size_t rows = std::min(16, nh / nkv);
-  return (size_t)PAT_MAX_BLOCKS * 2 * (8 + rows * (8 + (size_t)hd * 4));
+  return (size_t)PAT_MAX_BLOCKS * (8 + 2 * rows * (8 + (size_t)hd * 4));
 }
 
 // A number that no other call of this process has, and that what a workspace happens to hold
-// does not have either (64 bits would have to agree).
+// does not have either (48 bits would have to agree).
 inline unsigned long long paged_call_tag() {
   static std::atomic<unsigned long long> next{
       (unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count() ^
@@ -1243,7 +1239,7 @@ inline unsigned long long paged_call_tag() {
   z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
   z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
   z ^= z >> 31;
-  return z | 1;  // not 0, a clear flag
+  return z & ~PAT_COUNT;
 }
 
 // A pool as a 4-D tensor {head_dim, page_size, n_kv_heads, n_pages}; box: 16 tokens of one head
@@ -1287,13 +1283,15 @@ int paged_attention_inst(const LaunchCtx& c, const gpt2_paged_kv* kv, const Page
   pl.workers = grid * pl.warps;
   pl.qtiles = (pl.group + QR - 1) / QR;
   pl.items = a.c.nkv * pl.qtiles;
+  pl.per_item = 0xffffffffu / pl.items;
+  pl.per_worker = 0xffffffffu / pl.workers;
   pl.tag = paged_call_tag();
   char* p = static_cast<char*>(ws);
   pl.part = reinterpret_cast<float*>(p);  // every part a multiple of 16 bytes
   p += (size_t)grid * 2 * pl.rows * HD * 4;
   pl.ml = reinterpret_cast<float2*>(p);
   p += (size_t)grid * 2 * pl.rows * 8;
-  pl.flags = reinterpret_cast<unsigned long long*>(p);
+  pl.arrived = reinterpret_cast<unsigned long long*>(p);
   LaunchCtx cp = c;
   cp.pdl = true;
   const cudaError_t e = launch_k(cp, paged_attn_kernel<T, HD, QR, BOX>, dim3(grid), dim3(pl.warps * 32),

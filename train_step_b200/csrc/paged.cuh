@@ -47,7 +47,6 @@ struct PagedAppendArgs {
   const int* seqs;  // nullable: row n belongs to sequence n
   const float* cos_sin;
   int n_positions, rot;
-  int64_t row0;  // of this launch
   int tasks, tasks_per_row;
   uint32_t per_row, per_head;  // inverses of the tasks of a row and of a head, for paged_div_by
 };
@@ -90,7 +89,7 @@ __global__ void __launch_bounds__(PKV_THREADS, PKV_BLOCKS) paged_append_kernel(c
   const int step = gridDim.x * PKV_THREADS;
   for (int i = blockIdx.x * PKV_THREADS + threadIdx.x; i < a.tasks; i += step) {
     const int r = paged_div_by(i, a.tasks_per_row, a.per_row), t = i - r * a.tasks_per_row;
-    const int64_t n = a.row0 + r;
+    const int64_t n = r;
     int hh = paged_div_by(t, hp, a.per_head);
     const int j = t - hh * hp;
     // values are cut into the same pieces as keys
@@ -252,48 +251,25 @@ struct PatShape {
 struct PagedAttnPlan {
   int warps;    // of a block
   int workers, items, qtiles, group, rows;  // rows: min(QR, group), the rows of a partial result
-  unsigned long long tag;                   // of this call
-  unsigned long long* flags;                // [blocks][2]: see pat_arrive
+  uint32_t per_item, per_worker;            // inverses of items and workers, for paged_div_by
+  unsigned long long tag;                   // of this call, above the bits of PAT_COUNT
+  unsigned long long* arrived;              // [blocks]: see pat_claim
   float2* ml;                               // [blocks][2][rows]: maximum (log2 units) and sum
   float* part;                              // [blocks][2][rows][HD]
 };
 
-// The blocks b0..b1 that share an item each set a flag when their partial result is in the
-// workspace, then look at all of them; whoever sees them all set joins the item and clears them.
-// The fence between setting and looking makes at least one block see all (the one whose fence is
-// last); if two do, both write the same output. A flag is set when it holds the call's tag, so
-// the flags may hold anything before a call; they are clear after it, so that a captured call
-// may run again with the same tag. No block waits for another, and no atomic is contended (a
-// counter with compare-and-swap took a microsecond per block that arrived at the same time).
-// One warp calls this for the item that comes in from the block before (0) and the one that goes
-// on in the next (1), of blocks b0[i]..b1[i] (b0[i] < 0: none), after a barrier behind the block's
-// writes; last[i]: the block joins item i.
-__device__ __forceinline__ void pat_arrive(unsigned long long* flags, unsigned long long tag, const int (&b0)[2],
-                                           const int (&b1)[2], bool (&last)[2]) {
-  const int lane = threadIdx.x & 31;
-  if (lane == 0) {
-    __threadfence();
-#pragma unroll
-    for (int i = 0; i < 2; ++i)  // a block's flag of the item that begins in it is its second
-      if (b0[i] >= 0) *reinterpret_cast<volatile unsigned long long*>(flags + 2 * blockIdx.x + i) = tag;
-    asm volatile("fence.sc.gpu;" ::: "memory");
-  }
-  __syncwarp();
-  bool all[2] = {b0[0] >= 0, b0[1] >= 0};
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (b0[i] >= 0)
-      for (int b = b0[i] + lane; b <= b1[i]; b += 32) {
-        unsigned long long f;
-        asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(f) : "l"(flags + 2 * b + (b == b0[i])) : "memory");
-        all[i] &= f == tag;
-      }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    last[i] = __all_sync(0xffffffffu, all[i]);
-    if (last[i])
-      for (int b = b0[i] + lane; b <= b1[i]; b += 32) flags[2 * b + (b == b0[i])] = 0ull;
-  }
+// The blocks that share an item count their arrivals in the word of its first block; the last to
+// arrive joins the item. A word belongs to a call while it carries the call's tag: every block
+// that will arrive at a word claims it first (early, while it waits for its first tile, so that
+// nothing is spent on it later), whatever it holds; of several claims one succeeds, and no block
+// can have taken the last arrival before the others have claimed. The last one clears the word,
+// so that a captured call may run again with the same tag. No block waits for another.
+// (Measured and dropped: counting by compare-and-swap, a microsecond for each block that arrives
+// at the same time; a flag per block with a fence between setting and looking, 1.2 us more.)
+constexpr unsigned long long PAT_COUNT = 0xffffull;
+__device__ __forceinline__ void pat_claim(unsigned long long* word, unsigned long long tag) {
+  const unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+  if ((old & ~PAT_COUNT) != tag) atomicCAS(word, old, tag);
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
@@ -347,6 +323,20 @@ __device__ __forceinline__ void pat_prefix(const PagedAttnArgs& a, int* before) 
   }
   if (threadIdx.x == 0) before[0] = 0;
   __syncthreads();
+}
+
+// The place of tile u of the whole order. Every step of the search looks at 32 counts.
+__device__ __forceinline__ PagedCursor pat_locate(const int* before, int n_seqs, const PagedAttnPlan& pl, int64_t u) {
+  const int lane = threadIdx.x & 31;
+  const int r = u >> 31 ? (int)(u / pl.items) : paged_div_by((int)u, pl.items, pl.per_item);
+  int lo = 0, span = n_seqs;  // the sequence is one of lo ... lo + span - 1
+  while (span > 1) {
+    const int step = (span + 31) >> 5, at = lane * step;
+    const int k = __popc(__ballot_sync(0xffffffffu, at < span && before[lo + at] <= r)) - 1;
+    lo += k * step;
+    span = min(step, span - k * step);
+  }
+  return paged_place(before, lo, pl.items, u);
 }
 
 // The arithmetic of one worker on an item's tiles. Statistics are kept in log2 units (scores
@@ -569,10 +559,12 @@ struct PatWarp<float, HD, QR> {
     for (int r = 0; r < QR; ++r) {
       s[r] += __shfl_xor_sync(0xffffffffu, s[r], 16);
       s[r] = seen ? s[r] * scale_log2 : -INFINITY;
-      float t = s[r];
+      // as above, the maximum moves only when a score exceeds it by more than 8; most tiles need
+      // one vote per row and no reduction
+      if (__any_sync(0xffffffffu, s[r] > m[r] + 8.f)) {
+        float t = fmaxf(m[r], s[r]);
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-      if (t > m[r]) {  // the same for all lanes
+        for (int o = 1; o < 16; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
         const float f = exp2f(m[r] - t);
         m[r] = t;
         l[r] *= f;
@@ -701,7 +693,7 @@ struct PatSum {
 // threads, t = 0 ... threads - 1: a thread holds four elements of a row over every parts-th
 // block, with PAJ_AHEAD of them in flight. All threads of the block go through the barriers of
 // `rounds` rounds; `scratch` has 24 bytes per thread.
-constexpr int PAJ_AHEAD = 4;
+constexpr int PAJ_AHEAD = 8;
 template <class T, int HD>
 __device__ __forceinline__ void pat_join(const PagedAttnPlan& pl, int c0, int c1, int rows, T* out, float* lse,
                                          char* scratch, int t, int threads, int rounds) {
@@ -805,13 +797,13 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       }
   const int wb = blockIdx.x * pl.warps, we = wb + pl.warps - 1, w = wb + warp;  // the block's workers
   const int64_t total = (int64_t)before[B] * pl.items;
-  const int64_t share = paged_share(total, pl.workers);
+  const int64_t share = paged_share(total, pl.workers, pl.per_worker);
   const int64_t u0 = w * share, u1 = min(total, u0 + share);
   if (u0 < u1) {
     const int64_t n = u1 - u0;
     // copies: tile `pc`; the pages of its keys have been read a tile ahead (BOX: the one page, by
     // all lanes; otherwise the page of key `lane`, by the first 16)
-    PagedCursor pc = paged_locate(before, B, pl.items, u0);
+    PagedCursor pc = pat_locate(before, B, pl, u0);
     const PagedCursor first = pc;
     const int cap = a.c.max_pages << a.c.log2_page, slots = (1 << a.c.log2_page) - 1;
     int bad = 0, ignore = 0;
@@ -887,6 +879,11 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       if (!BOX) cp_async_commit();
     }
 
+    if (warp == 0 && lane == 0) {
+      // the words of the items that may come in and go on
+      pat_claim(pl.arrived + blockIdx.x, pl.tag);
+      if (first.tile > 0) pat_claim(pl.arrived + (int)paged_div(u0 - first.tile, share) / pl.warps, pl.tag);
+    }
     PagedCursor c = first;
     const float scale_log2 = a.scale * 1.4426950408889634f;
     PatWarp<T, HD, QR> pw(side);
@@ -969,10 +966,14 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   // a thread joins four elements of a split item's row over the block's pieces
   constexpr int VEC = HD / 4;
   const int cols = pl.rows * VEC, bytes = S::warp_bytes(pl.rows), tail = S::head(pl.rows);
-  for (int i = threadIdx.x; i < (pl.warps + 1) * cols; i += blockDim.x) {
-    const int k = i / cols, col = i - k * cols, row = col / VEC, v = col - row * VEC;
+  const uint32_t there = __ballot_sync(0xffffffffu, lane <= pl.warps && s_split[min(lane, pl.warps)].seq >= 0);
+  for (int i = threadIdx.x; i < __popc(there) * cols; i += blockDim.x) {
+    const int nth = i / cols, col = i - nth * cols, row = col / VEC, v = col - row * VEC;
+    uint32_t left = there;  // without its first nth
+    for (int j = 0; j < nth; ++j) left &= left - 1;
+    const int k = __ffs(left) - 1;
     const Split sp = s_split[k];
-    if (sp.seq < 0 || row >= sp.rows) continue;
+    if (row >= sp.rows) continue;
     PatSum sum;
     for (int p = sp.p0; p <= sp.p1; p += 4) {
       float2 ml[4];
@@ -1000,21 +1001,19 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   }
   if (s_cross[0] < 0 && s_cross[1] < 0) return;
   __syncthreads();
-  if (warp == 0) {
-    int b0[2], b1[2];
-    bool last[2];
+  if (threadIdx.x == 0) {
+    __threadfence();  // the block's partial results, before its arrivals
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      b0[i] = b1[i] = -1;
       if (s_cross[i] < 0) continue;
-      b0[i] = s_split[s_cross[i]].b0;
-      b1[i] = s_split[s_cross[i]].b1;
+      const Split sp = s_split[s_cross[i]];
+      unsigned long long* word = pl.arrived + sp.b0;
+      const unsigned long long old = atomicAdd(word, 1ull);
+      if ((int)(old & PAT_COUNT) != sp.b1 - sp.b0) continue;
+      s_last[i] = 1;
+      *word = 0ull;
     }
-    pat_arrive(pl.flags, pl.tag, b0, b1, last);
-    if (lane == 0) {
-      s_last[0] = last[0];
-      s_last[1] = last[1];
-    }
+    __threadfence();  // those of the blocks that arrived before
   }
   __syncthreads();
   if (!s_last[0] && !s_last[1]) return;

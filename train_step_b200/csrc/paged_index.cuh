@@ -67,8 +67,10 @@ G2_HD int paged_div_by(int x, int d, uint32_t inverse) {
   const int q = (int)(((uint64_t)(uint32_t)x * inverse) >> 32);
   return q + (x - q * d >= d);
 }
-G2_HD int64_t paged_share(int64_t total, int workers) {
-  const int64_t s = paged_div(total + workers - 1, workers);
+// The share of each of `workers`: total / workers, rounded up; `inverse` as in paged_div_by.
+G2_HD int64_t paged_share(int64_t total, int workers, uint32_t inverse) {
+  const int64_t x = total + workers - 1;
+  const int64_t s = x >> 31 ? x / workers : paged_div_by((int)x, workers, inverse);
   return s < 1 ? 1 : s;
 }
 
@@ -78,21 +80,12 @@ struct PagedCursor {
   int seq, item, tile, tiles;
 };
 
-// The place of tile u of the whole order, 0 <= u < items * before[n_seqs].
-G2_HD PagedCursor paged_locate(const int* before, int n_seqs, int items, int64_t u) {
-  const int r = (int)paged_div(u, items);  // the sequence with before[seq] <= r < before[seq + 1]
-  int lo = 0, hi = n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (before[mid] <= r)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
+// The place of tile u, which is one of sequence `seq`'s.
+G2_HD PagedCursor paged_place(const int* before, int seq, int items, int64_t u) {
   PagedCursor c;
-  c.seq = lo;
-  c.tiles = before[lo + 1] - before[lo];
-  const int64_t v = u - (int64_t)before[lo] * items;
+  c.seq = seq;
+  c.tiles = before[seq + 1] - before[seq];
+  const int64_t v = u - (int64_t)before[seq] * items;
   c.item = (int)paged_div(v, c.tiles);
   c.tile = (int)(v - (int64_t)c.item * c.tiles);
   return c;
