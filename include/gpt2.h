@@ -443,7 +443,7 @@ int gpt2_op_sample_topk(const float* logits, int64_t ld, int rows, int V, int k,
  * status (nullable): int32 device word, zero at first. Contents of device memory cannot be
  * checked by the host: a page id outside [0, n_pages), a sequence, position or length outside
  * the cache is not followed, the access is skipped as documented at each call, and the word
- * is raised; gpt2_op_paged_status reports it.
+ * is raised (as it is by a bounded wait that gave up); gpt2_op_paged_status reports it.
  * The struct is read during the call only. */
 typedef struct {
   void *k, *v;
@@ -461,7 +461,8 @@ typedef struct {
  * the table f32_cos_sin [n_positions][rot_dim] (16-byte aligned; row t: the rot_dim/2 cosines,
  * then the sines, of position t): the pair (x, y) of elements (i, i + rot_dim/2), or (2i,
  * 2i + 1) when interleaved != 0, becomes (x c_i - y s_i, x s_i + y c_i), computed in fp32 and
- * rounded once; elements from rot_dim on are copied. q (nullable, with q_out and n_q_heads):
+ * rounded once; elements from rot_dim on are copied. N times the vectors of a row is limited
+ * (GPT2_ERR_BATCH): N * (n_q_heads + 2 n_kv_heads) * head_dim elements of at most 32 GB. q (nullable, with q_out and n_q_heads):
  * query rows of the same tokens, rotated the same way into q_out (may be q itself, with the
  * same row stride). A row whose position, sequence, table entry or rotation row is outside
  * its range is skipped and raises the status word; rows that are skipped leave q_out as it
@@ -481,8 +482,9 @@ int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const void* k, int64_t ldk,
  * f32_lse (nullable): [n_seqs][n_q_heads], the natural logarithm of the sum of exponentials.
  * L = 0 gives out = 0 and lse = -inf. A length outside [0, max_pages*page_size] is brought to
  * the nearer end, a key whose page id is bad is left out, and both raise the status word.
- * Softmax statistics and sums are fp32, each output is rounded once. out may not overlap q,
- * the cache or ws. ws: DEVICE workspace of gpt2_paged_attention_ws_bytes bytes, 16-byte
+ * Softmax statistics and sums are fp32, each output is rounded once; a NaN in q, or in a
+ * visible key or value, gives NaN where the formula does, one in an unseen place has no effect.
+ * 0 < scale <= 1e38. out may not overlap q, the cache or ws. ws: DEVICE workspace of gpt2_paged_attention_ws_bytes bytes, 16-byte
  * aligned, of any content; calls that may run at the same time need one each.
  * Deterministic for given lengths. */
 int gpt2_op_paged_attention(const gpt2_paged_kv* kv, const void* q, int64_t ldq, int n_q_heads,
@@ -493,8 +495,9 @@ int gpt2_op_paged_attention(const gpt2_paged_kv* kv, const void* q, int64_t ldq,
 size_t gpt2_paged_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim);
 
 /* Wait for `stream`, read and clear the cache's status word: GPT2_ERR_PAGE_RANGE if a call on
- * the cache met a bad page id, sequence, position or length since it was last cleared.
- * GPT2_ERR_CONFIG for a cache without one. */
+ * the cache met a bad page id, sequence, position or length since it was last cleared,
+ * GPT2_ERR_TIMEOUT if a wait gave up (its results are void). GPT2_ERR_CONFIG for a cache
+ * without one. */
 int gpt2_op_paged_status(const gpt2_paged_kv* kv, void* stream);
 
 /* Check of the device-side timeout path (no counterpart on the pages: it tests the

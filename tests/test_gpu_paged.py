@@ -233,6 +233,51 @@ def test_attention_row_strides_and_optional_outputs(dtype):
     assert (got[:, :2] == 7).all() and (got[:, 6:] == 7).all()
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("n", [10, 5000])  # within one worker, and spread over many
+def test_attention_passes_on_nan(dtype, n):
+    kv, q, ln, out, lse, ref = attention_case([n, 33], 4, 2, 64, 16, dtype, "heads", seed=31, poison=False)
+    q[0, 1] = math.nan  # one query: its row alone
+    got, l2 = torch.empty_like(out), torch.empty_like(lse)
+    tsb.paged_attention(kv, q, ln, got, lse=l2)
+    assert torch.isnan(got[0, 1]).all() and torch.isnan(l2[0, 1])
+    keep = torch.ones(2, 4, dtype=torch.bool, device="cuda")
+    keep[0, 1] = False
+    assert torch.equal(got[keep], out[keep]) and torch.equal(l2[keep], lse[keep])
+    q[0, 1] = 0
+    pg = int(kv.page_table[0, (n - 1) // 16])
+    kv.v_cache[pg, (n - 1) % 16, 1, 5] = math.nan  # one element of a value: that element of its heads
+    tsb.paged_attention(kv, q, ln, got)
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[0, 2:, 5] = True
+    assert torch.equal(torch.isnan(got), bad)
+    kv.k_cache[pg, (n - 1) % 16, 1, 5] = math.nan  # a key: all of its heads
+    tsb.paged_attention(kv, q, ln, got, lse=l2)
+    bad[0, 2:] = True
+    assert torch.equal(torch.isnan(got), bad) and torch.isnan(l2[0, 2:]).all() and not torch.isnan(l2[0, :2]).any()
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("page", [8, 16, 64])
+def test_attention_over_an_expanded_cache(dtype, page):
+    # one stored head shown as four (head stride 0)
+    g = torch.Generator().manual_seed(17)
+    rng = np.random.default_rng(17)
+    lens = [100, 1, 37]
+    table, pages = tables(lens, page, 1, rng)
+    kc, vc = (pool(pages, page, 1, 64, dtype, "tokens", g).expand(-1, -1, 4, -1) for _ in range(2))
+    q = torch.randn(3, 8, 64, generator=g).to(dtype).cuda()
+    kv = tsb.PagedKV(kc, vc, torch.from_numpy(table).cuda())
+    out, lse = torch.empty_like(q), torch.empty(3, 8, device="cuda")
+    tsb.paged_attention(kv, q, torch.tensor(lens, dtype=torch.int32).cuda(), out, lse=lse)
+    kv.check()
+    check(out, lse, reference(kc.double().cpu(), vc.double().cpu(), table, q.double().cpu(), lens, 0.125), dtype)
+
+
+def test_attention_of_the_most_sequences():
+    attention_case([(i * 29) % 23 for i in range(4096)], 2, 1, 32, 16, torch.bfloat16, "heads", seed=41)
+
+
 def test_attention_offsets_beyond_32_bits():
     # two pages more than 2^32 bytes and 2^31 elements apart, in caches of 4.5 GB
     page, nkv, hd = 16, 1, 64
@@ -457,6 +502,9 @@ def test_bindings_refuse():
                 dict(ws=torch.zeros(1 << 26, dtype=torch.uint8))):
         with pytest.raises(ValueError):
             tsb.paged_attention(kv, **{**dict(q=q, seq_lens=n, out=out), **bad})
+    for bad in (dict(window=-1), dict(window=2 ** 32 + 5), dict(sinks=-1), dict(sinks=2 ** 31)):
+        with pytest.raises(ValueError):
+            tsb.paged_attention(kv, q, n, out, **bad)
     with pytest.raises(ValueError):  # an explicit stream needs its own workspace
         tsb.paged_attention(kv, q, n, out, stream=torch.cuda.current_stream().cuda_stream)
     with pytest.raises(tsb.Gpt2Error):
@@ -554,6 +602,31 @@ def test_captured_step_replays_with_new_lengths(dtype):
         tsb.paged_attention(kv, qr, lens, want)
         assert torch.equal(out, want) and torch.equal(out2, want)
     kv.check()
+
+
+def test_captured_calls_share_a_workspace_in_turn():
+    kv, q, ln, out, lse, _ = attention_case([3000, 10, 700], 8, 2, 64, 16, torch.bfloat16, "heads", seed=22)
+    ws = kv.attention_workspace(8)
+    # the second reads past the third sequence's tokens, into NaN and bad pages: the same each time
+    lens = [ln] + [torch.tensor(n, dtype=torch.int32).cuda() for n in ([77, 0, 2999], [500, 3, 650])]
+    want = [out] + [torch.empty_like(out) for _ in lens[1:]]
+    for n, o in zip(lens[1:], want[1:]):
+        tsb.paged_attention(kv, q, n, o)
+    assert torch.isfinite(want[2].float()).all()
+    outs, graphs = [torch.empty_like(out) for _ in lens], []
+    for o, n in zip(outs, lens):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            tsb.paged_attention(kv, q, n, o, ws=ws)
+            tsb.paged_attention(kv, q, n, o, ws=ws)
+        graphs.append(gr)
+    for fill in (None, 85, 255):
+        if fill is not None:
+            ws.fill_(fill)
+        for which in (0, 0, 1, 2, 0, 2, 2, 1, 1, 0):
+            outs[which].zero_()
+            graphs[which].replay()
+            assert torch.equal(outs[which].view(torch.int16), want[which].view(torch.int16))
 
 
 def test_calls_on_other_streams():

@@ -76,7 +76,7 @@ def test_a_null_cache_is_refused():
     (dict(nh=-1), CONFIG), (dict(nh=5000, ldq=320000, ldqo=320000), CONFIG), (dict(ldq=248), CONFIG),
     (dict(ldqo=260), CONFIG), (dict(q_out=A + 4), CONFIG), (dict(N=-1), CONFIG), (dict(positions=None), CONFIG),
     (dict(seqs=None, N=4), BATCH), (dict(N=1 << 29), BATCH), (dict(rot=8), CONFIG), (dict(rot=80), CONFIG), (dict(rot=-16), CONFIG),
-    (dict(cos_sin=None), CONFIG), (dict(cos_sin=A + 4), CONFIG), (dict(n_positions=0), CONFIG),
+    (dict(positions=A + 2), CONFIG), (dict(seqs=A + 1), CONFIG), (dict(cos_sin=None), CONFIG), (dict(cos_sin=A + 4), CONFIG), (dict(n_positions=0), CONFIG),
 ])
 def test_append_refuses(change, code):
     assert append(cache(), **change) == code
@@ -91,7 +91,7 @@ def test_append_of_no_rows_does_nothing():
 @pytest.mark.parametrize("change,code", [
     (dict(q=None), CONFIG), (dict(out=None), CONFIG), (dict(q=A + 8), CONFIG), (dict(ldq=248), CONFIG),
     (dict(ldo=252), CONFIG), (dict(nh=0), CONFIG), (dict(nh=3), CONFIG), (dict(nh=4098), CONFIG),
-    (dict(lens=None), CONFIG), (dict(scale=0.0), CONFIG), (dict(scale=-1.0), CONFIG),
+    (dict(lens=None), CONFIG), (dict(lens=A + 2), CONFIG), (dict(lse=A + 3), CONFIG), (dict(scale=2e38), CONFIG), (dict(scale=0.0), CONFIG), (dict(scale=-1.0), CONFIG),
     (dict(scale=float("nan")), CONFIG), (dict(scale=float("inf")), CONFIG), (dict(window=-1), CONFIG),
     (dict(sinks=-1), CONFIG), (dict(ws=None), CONFIG), (dict(ws=A + 8), CONFIG), (dict(ws_bytes=0), CONFIG),
 ])

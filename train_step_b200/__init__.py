@@ -723,6 +723,8 @@ def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None
                 or not lse.is_contiguous()):
             raise ValueError(f"lse must be a contiguous fp32 tensor [{B}, {nh}] on {cache.device}")
         pl = lse.data_ptr()
+    if not (0 <= window < 2 ** 31 and 0 <= sinks < 2 ** 31):
+        raise ValueError("window and sinks must be in [0, 2^31)")
     if ws is None:
         if stream is not None:
             raise ValueError("a call on an explicit stream needs its own workspace")

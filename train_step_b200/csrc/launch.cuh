@@ -1186,7 +1186,8 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedApp
   if (r) return r;
   if (a.rows < 0 || a.nh < 0) return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: negative size");
   if (a.rows == 0) return GPT2_OK;
-  if (!a.positions) return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: positions are required");
+  if (!a.positions || ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.seqs)) & 3))
+    return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: positions are required; they and seqs must be 4-byte aligned");
   if (a.nh > 4096) return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: at most 4096 query heads");
   if (!a.seqs && a.rows > kv->n_seqs)
     return fail(c, GPT2_ERR_BATCH, "paged_kv_append: more rows than sequences (and no sequence indices)");
@@ -1319,10 +1320,11 @@ inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedAtt
   if (r) return r;
   if (!paged_heads_ok(a.nh, a.c.nkv))
     return fail(c, GPT2_ERR_CONFIG, "paged_attention: n_q_heads must be a multiple of n_kv_heads, at most 4096");
-  if (!(a.scale > 0.f) || a.scale > 3.4e38f || a.window < 0 || a.sinks < 0)
-    return fail(c, GPT2_ERR_CONFIG, "paged_attention: finite scale > 0, window >= 0, sinks >= 0");
+  if (!(a.scale > 0.f) || !(a.scale <= 1e38f) || a.window < 0 || a.sinks < 0)
+    return fail(c, GPT2_ERR_CONFIG, "paged_attention: 0 < scale <= 1e38, window >= 0, sinks >= 0");
   if (kv->n_seqs == 0) return GPT2_OK;
-  if (!a.lens) return fail(c, GPT2_ERR_CONFIG, "paged_attention: seq_lens are required");
+  if (!a.lens || ((reinterpret_cast<uintptr_t>(a.lens) | reinterpret_cast<uintptr_t>(a.lse)) & 3))
+    return fail(c, GPT2_ERR_CONFIG, "paged_attention: seq_lens are required; they and lse must be 4-byte aligned");
   const int vn = kv->dtype == GPT2_BF16 ? 8 : 4, hd = kv->head_dim;
   if (!paged_rows_ok(a.q, a.ldq, a.nh, hd, vn) || !paged_rows_ok(a.out, a.ldo, a.nh, hd, vn))
     return fail(c, GPT2_ERR_CONFIG,

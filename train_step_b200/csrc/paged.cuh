@@ -188,20 +188,26 @@ struct PagedAttnArgs {
 // contiguous share of them, so ragged lengths balance without the host knowing them. A worker
 // that takes an item whole writes its output. Otherwise it leaves pieces in shared memory: at
 // most one that begins inside an item (its head piece) and one that begins with an item and does
-// not reach its end (its tail piece). When a block's workers are done, a warp joins the pieces
+// not reach its end (its tail piece). When a block's workers are done, the block joins the pieces
 // of each split item: to its output, or, for an item spread over several blocks, to a partial
 // result in the workspace (at most two per block: of the item that comes in from the block
 // before, slot 0, and of the one that goes on in the next, slot 1). The block that arrives last
 // at such an item joins its partial results, in their order, so results do not depend on the
-// order of arrival.
+// order of arrival. (A second kernel for the join cost 3 us more per call.)
 // A worker streams its tiles through a ring of its own in shared memory, STAGES tiles ahead and
 // on into the next item (the queries of an item arrive with its first tile); it needs no barrier
 // but its own mbarriers and the warp's. With pages of 16 tokens or more (BOX) a tile is one
 // rectangle of a page and arrives by tensor copies that one lane issues; smaller pages, and
 // strides that a tensor map does not take, go through 16-byte copies by all lanes.
-// What bounds it: reading the cache from HBM, and, before that, the instructions of a warp (few
-// warps per scheduler, each a chain of dependent steps): 16-byte copies by all lanes took half
-// of a tile's instructions, which is what the tensor copies save.
+// What bounds it. Long caches: reading them from HBM; 128 sequences of 512 to 8,192 tokens with 8
+// key heads of 128 (1.46 GB) take 238 us, 6.1 TB/s, where a kernel that only reads as many random
+// pages in equal shares reaches 6.6 TB/s. Before that it was the instructions of a warp: two or
+// three warps per scheduler, each a chain of dependent steps, of which 16-byte copies by all
+// lanes were half (300 us). Short ones: the chain of lengths, place, page, copy, first tile
+// (4 us) and, when items cross blocks, arrival and join (4 us): 16 sequences of 1,024 tokens, 12
+// heads of 64 (50 MB) take 17.6 us, of which 7 us stream.
+// Pages that keep each head's tokens together read faster than pages of whole tokens (25 heads
+// of 64: 95 % and 77 % of the copy rate), whose rows of 128 bytes are far apart.
 constexpr int PAT_MAX_BLOCKS = 256;
 constexpr int PAT_SMEM = 226 * 1024;  // of a block
 
@@ -351,8 +357,8 @@ struct PatWarp;
 // two halves of the result are added at the end; with up to 16 heads the remainders take a
 // second product. P is so carried to 2^-16 of its value at no or little cost (the products
 // are far from the tensor cores' rate: the kernel is bound by reading the cache).
-// The running maximum moves only when a tile exceeds it by more than 8 (weights stay below
-// 2^8, exact enough in fp32), so most tiles do not rescale the output.
+// The running maximum moves only when a tile exceeds it by more than 8 (weights and sums against
+// an older maximum are at most 2^8 larger, and as exact), so most tiles do not rescale the output.
 template <int HD, int QR>
 struct PatWarp<bf16, HD, QR> {
   using S = PatShape<bf16, HD, QR>;
@@ -510,7 +516,9 @@ struct PatWarp<bf16, HD, QR> {
 
 // fp32: fp32 products and sums. Scores: a lane has a key and half of the elements; weights go
 // to the P V loop through shared memory, where a lane holds HD/32 output elements (neighbours,
-// or 32 apart for HD 96).
+// or 32 apart for HD 96). One query head per key head is bound by HBM (12 heads of 64: 92 % of
+// the copy rate); with 4 and 8 the shared-memory reads of queries and weights bound it (62 % and
+// 44 %; packed pairs of fp32 products were slower for the moves they need).
 template <int HD, int QR>
 struct PatWarp<float, HD, QR> {
   using S = PatShape<float, HD, QR>;
@@ -657,8 +665,8 @@ struct PatSum {
     float mn = m;
 #pragma unroll
     for (int i = 0; i < N; ++i) mn = fmaxf(mn, ml[i].x);
-    if (mn == -INFINITY) return;  // nothing visible so far
-    const float f = ex2_fast(m - mn);
+    const float ref = mn == -INFINITY ? 0.f : mn;  // nothing visible so far: the weights are 0
+    const float f = ex2_fast(m - ref);
     m = mn;
     l *= f;
     o.x *= f;
@@ -667,7 +675,7 @@ struct PatSum {
     o.w *= f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float g = ex2_fast(ml[i].x - mn);
+      const float g = ex2_fast(ml[i].x - ref);
       l = fmaf(ml[i].y, g, l);
       o.x = fmaf(x[i].x, g, o.x);
       o.y = fmaf(x[i].y, g, o.y);
