@@ -266,16 +266,18 @@ struct PagedAttnPlan {
 
 // The blocks that share an item count their arrivals in the word of its first block; the last to
 // arrive joins the item. A word belongs to a call while it carries the call's tag: every block
-// that will arrive at a word claims it first (early, while it waits for its first tile, so that
-// nothing is spent on it later), whatever it holds; of several claims one succeeds, and no block
-// can have taken the last arrival before the others have claimed. The last one clears the word,
+// that will arrive at a word claims it first (early, and read earlier still, so that nothing waits
+// for it), whatever it holds; of several claims one succeeds, and no block can have taken the
+// last arrival before the others have claimed. The last one clears the word,
 // so that a captured call may run again with the same tag. No block waits for another.
 // (Measured and dropped: counting by compare-and-swap, a microsecond for each block that arrives
 // at the same time; a flag per block with a fence between setting and looking, 1.2 us more.)
 constexpr unsigned long long PAT_COUNT = 0xffffull;
-__device__ __forceinline__ void pat_claim(unsigned long long* word, unsigned long long tag) {
-  const unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
-  if ((old & ~PAT_COUNT) != tag) atomicCAS(word, old, tag);
+__device__ __forceinline__ unsigned long long pat_look(const unsigned long long* word) {
+  return *reinterpret_cast<const volatile unsigned long long*>(word);
+}
+__device__ __forceinline__ void pat_claim(unsigned long long* word, unsigned long long seen, unsigned long long tag) {
+  if ((seen & ~PAT_COUNT) != tag) atomicCAS(word, seen, tag);
 }
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
@@ -794,6 +796,10 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   }
   pdl_launch_dependents();
   pdl_wait();  // nothing above touches global memory
+  // the arrival words of the items that may go on (0) and come in (1), by the block's first thread
+  unsigned long long* word[2] = {pl.arrived + blockIdx.x, nullptr};
+  unsigned long long seen_word[2] = {0ull, 0ull};
+  if (threadIdx.x == 0) seen_word[0] = pat_look(word[0]);
   pat_prefix(a, before);
   const int B = a.c.n_seqs;
   // sequences without tokens
@@ -813,6 +819,10 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
     // all lanes; otherwise the page of key `lane`, by the first 16)
     PagedCursor pc = pat_locate(before, B, pl, u0);
     const PagedCursor first = pc;
+    if (threadIdx.x == 0 && first.tile > 0) {
+      word[1] = pl.arrived + (int)paged_div(u0 - first.tile, share) / pl.warps;
+      seen_word[1] = pat_look(word[1]);
+    }
     const int cap = a.c.max_pages << a.c.log2_page, slots = (1 << a.c.log2_page) - 1;
     int bad = 0, ignore = 0;
     PagedVisible vis = paged_visible(paged_length(a.lens[pc.seq], cap, &ignore), a.window, a.sinks);
@@ -887,10 +897,9 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       if (!BOX) cp_async_commit();
     }
 
-    if (warp == 0 && lane == 0) {
-      // the words of the items that may come in and go on
-      pat_claim(pl.arrived + blockIdx.x, pl.tag);
-      if (first.tile > 0) pat_claim(pl.arrived + (int)paged_div(u0 - first.tile, share) / pl.warps, pl.tag);
+    if (threadIdx.x == 0) {
+      pat_claim(word[0], seen_word[0], pl.tag);
+      if (word[1]) pat_claim(word[1], seen_word[1], pl.tag);
     }
     PagedCursor c = first;
     const float scale_log2 = a.scale * 1.4426950408889634f;
