@@ -301,8 +301,27 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// before[b] = tiles per item of sequences 0..b-1, for b <= n_seqs (whole block).
+// before[b] = tiles per item of sequences 0..b-1, for b <= n_seqs (whole block). Up to 32
+// sequences: every warp writes all of the same counts, and waits for nobody.
 __device__ __forceinline__ void pat_prefix(const PagedAttnArgs& a, int* before) {
+  if (a.c.n_seqs <= 32) {
+    const int lane = threadIdx.x & 31;
+    int bad = 0, n = 0;
+    if (lane < a.c.n_seqs) {
+      n = paged_length(a.lens[lane], a.c.max_pages << a.c.log2_page, &bad);
+      n = paged_visible(n, a.window, a.sinks).tiles;
+    }
+    if (bad && blockIdx.x == 0 && threadIdx.x < 32) raise_device_error(a.c.status, DEV_PAGE_RANGE);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += v;
+    }
+    if (lane < a.c.n_seqs) before[lane + 1] = n;
+    if (lane == 0) before[0] = 0;
+    __syncwarp();
+    return;
+  }
   __shared__ int wsum[32];
   const int threads = blockDim.x, B = a.c.n_seqs, per = (B + threads - 1) / threads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -795,7 +814,8 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
     }
   }
   pdl_launch_dependents();
-  pdl_wait();  // nothing above touches global memory
+  __syncthreads();  // the shared words are set
+  pdl_wait();       // nothing above touches global memory
   // the arrival words of the items that may go on (0) and come in (1), by the block's first thread
   unsigned long long* word[2] = {pl.arrived + blockIdx.x, nullptr};
   unsigned long long seen_word[2] = {0ull, 0ull};
