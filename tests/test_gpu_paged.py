@@ -165,6 +165,22 @@ def test_attention_long_and_ragged(dtype, hd, NH, nkv):
     attention_case([20000] + [1 + 7 * i for i in range(40)], NH, nkv, hd, 32, dtype, "heads", seed=5)
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("hd,NH,nkv,page", [(32, 6, 2, 16), (64, 16, 1, 8), (64, 40, 2, 16), (96, 9, 1, 64),
+                                            (96, 5, 1, 4), (128, 16, 2, 32), (128, 12, 1, 16), (128, 3, 3, 2)])
+def test_attention_of_items_spread_over_blocks(dtype, hd, NH, nkv, page):
+    # items too large for one block, next to empty and small ones; several orders of the lengths
+    lens = [1500, 1, 40, 0, 2100]
+    for k in range(2):
+        attention_case(lens[k:] + lens[:k], NH, nkv, hd, page, dtype, "heads", seed=hd + page + k)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("window,sinks", [(1200, 0), (1200, 20), (1111, 1000), (3, 2500)])
+def test_attention_through_large_windows(dtype, window, sinks):
+    attention_case([5000, 1100, 77, 3001], 4, 2, 64, 16, dtype, "heads", window, sinks, seed=window)
+
+
 def test_attention_more_sequences_than_workers():
     attention_case([(i * 13) % 40 for i in range(700)], 5, 5, 32, 8, torch.bfloat16, "heads", seed=8)
 

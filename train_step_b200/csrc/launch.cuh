@@ -1286,6 +1286,7 @@ int paged_attention_inst(const LaunchCtx& c, const gpt2_paged_kv* kv, const Page
   pl.items = a.c.nkv * pl.qtiles;
   pl.per_item = 0xffffffffu / pl.items;
   pl.per_worker = 0xffffffffu / pl.workers;
+  pl.per_block = 0xffffffffu / grid;
   pl.tag = paged_call_tag();
   char* p = static_cast<char*>(ws);
   pl.part = reinterpret_cast<float*>(p);  // every part a multiple of 16 bytes

@@ -234,11 +234,14 @@ struct PatShape {
     return (head(rows) + piece(rows) + SIDE + STAGES * 12 + 1023) / 1024 * 1024;
   }
   // workers of a block: as many as fit beside the n_seqs + 1 counts (the first 1024 bytes align
-  // the rest)
+  // the rest), in equal numbers for the SM's four schedulers where there are two or three each
+  // (8 for 10 that fit: 92.5 -> 88.5 us for one sequence of 131,071 tokens)
   static constexpr int warps(int rows, int n_seqs) {
     const int fit = (PAT_SMEM - 1024 - (n_seqs + 1) * 4) / warp_bytes(rows);
-    return fit > 12 ? 12 : fit;
+    return fit >= 12 ? 12 : fit >= 8 ? 8 : fit;
   }
+  // an item of at most so many tiles (128 KB of keys and values) is not split between blocks
+  static constexpr int WHOLE = 131072 / (2 * TILE);
   static constexpr int smem(int rows, int n_seqs) {
     return 1024 + warps(rows, n_seqs) * warp_bytes(rows) + (n_seqs + 1) * 4;
   }
@@ -257,7 +260,7 @@ struct PatShape {
 struct PagedAttnPlan {
   int warps;    // of a block
   int workers, items, qtiles, group, rows;  // rows: min(QR, group), the rows of a partial result
-  uint32_t per_item, per_worker;            // inverses of items and workers, for paged_div_by
+  uint32_t per_item, per_worker, per_block; // inverses of items, workers and blocks, for paged_div_by
   unsigned long long tag;                   // of this call, above the bits of PAT_COUNT
   unsigned long long* arrived;              // [blocks]: see pat_claim
   float2* ml;                               // [blocks][2][rows]: maximum (log2 units) and sum
@@ -301,9 +304,10 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// before[b] = tiles per item of sequences 0..b-1, for b <= n_seqs (whole block). Up to 32
-// sequences: every warp writes all of the same counts, and waits for nobody.
-__device__ __forceinline__ void pat_prefix(const PagedAttnArgs& a, int* before) {
+// before[b] = tiles per item of sequences 0..b-1, for b <= n_seqs (whole block); returns the
+// largest number of tiles of an item. Up to 32 sequences: every warp writes all of the same
+// counts, and waits for nobody.
+__device__ __forceinline__ int pat_prefix(const PagedAttnArgs& a, int* before) {
   if (a.c.n_seqs <= 32) {
     const int lane = threadIdx.x & 31;
     int bad = 0, n = 0;
@@ -312,6 +316,7 @@ __device__ __forceinline__ void pat_prefix(const PagedAttnArgs& a, int* before) 
       n = paged_visible(n, a.window, a.sinks).tiles;
     }
     if (bad && blockIdx.x == 0 && threadIdx.x < 32) raise_device_error(a.c.status, DEV_PAGE_RANGE);
+    const int most = __reduce_max_sync(0xffffffffu, n);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, n, o);
@@ -320,19 +325,21 @@ __device__ __forceinline__ void pat_prefix(const PagedAttnArgs& a, int* before) 
     if (lane < a.c.n_seqs) before[lane + 1] = n;
     if (lane == 0) before[0] = 0;
     __syncwarp();
-    return;
+    return most;
   }
-  __shared__ int wsum[32];
+  __shared__ int wsum[32], wmax[32];
   const int threads = blockDim.x, B = a.c.n_seqs, per = (B + threads - 1) / threads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cap = a.c.max_pages << a.c.log2_page;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
-  int sum = 0, bad = 0;
+  int sum = 0, most = 0, bad = 0;
   for (int b = b0; b < b1; ++b) {
     const int n = paged_visible(paged_length(a.lens[b], cap, &bad), a.window, a.sinks).tiles;
     before[b + 1] = n;
     sum += n;
+    most = max(most, n);
   }
+  most = __reduce_max_sync(0xffffffffu, most);
   if (bad && blockIdx.x == 0) raise_device_error(a.c.status, DEV_PAGE_RANGE);
   int inc = sum;
 #pragma unroll
@@ -340,8 +347,12 @@ __device__ __forceinline__ void pat_prefix(const PagedAttnArgs& a, int* before) 
     const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
-  if (lane == 31) wsum[warp] = inc;
+  if (lane == 31) {
+    wsum[warp] = inc;
+    wmax[warp] = most;
+  }
   __syncthreads();
+  for (int w = 0; w < threads / 32; ++w) most = max(most, wmax[w]);
   int base = inc - sum;
   for (int w = 0; w < warp; ++w) base += wsum[w];
   for (int b = b0; b < b1; ++b) {
@@ -350,6 +361,7 @@ __device__ __forceinline__ void pat_prefix(const PagedAttnArgs& a, int* before) 
   }
   if (threadIdx.x == 0) before[0] = 0;
   __syncthreads();
+  return most;
 }
 
 // The place of tile u of the whole order. Every step of the search looks at 32 counts.
@@ -364,6 +376,14 @@ __device__ __forceinline__ PagedCursor pat_locate(const int* before, int n_seqs,
     span = min(step, span - k * step);
   }
   return paged_place(before, lo, pl.items, u);
+}
+
+// The first tile of an item at or after tile u, 0 <= u <= total.
+__device__ __forceinline__ int64_t pat_item_start(const int* before, int n_seqs, const PagedAttnPlan& pl, int64_t u,
+                                                  int64_t total) {
+  if (u >= total) return total;
+  const PagedCursor c = pat_locate(before, n_seqs, pl, u);
+  return c.tile == 0 ? u : u + (c.tiles - c.tile);
 }
 
 // The arithmetic of one worker on an item's tiles. Statistics are kept in log2 units (scores
@@ -789,6 +809,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   __shared__ int s_cross[2];  // which of them other blocks share: the one that comes in, that goes on (-1: none)
   __shared__ int s_last[2];   // this block is the last to arrive at it
   __shared__ int s_no_abort;
+  __shared__ int64_t s_edge[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   char* ring = pat_smem + warp * S::warp_bytes(pl.rows);
   char* head = ring + S::head(pl.rows);
@@ -820,7 +841,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   unsigned long long* word[2] = {pl.arrived + blockIdx.x, nullptr};
   unsigned long long seen_word[2] = {0ull, 0ull};
   if (threadIdx.x == 0) seen_word[0] = pat_look(word[0]);
-  pat_prefix(a, before);
+  const int most = pat_prefix(a, before);
   const int B = a.c.n_seqs;
   // sequences without tokens
   for (int b = blockIdx.x; b < B; b += gridDim.x)
@@ -829,10 +850,29 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
         static_cast<T*>(a.out)[b * a.ldo + i] = from_f32<T>(0.f);
         if (a.lse && i < a.nh) a.lse[(int64_t)b * a.nh + i] = -INFINITY;
       }
-  const int wb = blockIdx.x * pl.warps, we = wb + pl.warps - 1, w = wb + warp;  // the block's workers
+  // the block's tiles [a0, a1), of which each of its warps takes `share`: equal ranges, or, when
+  // every item is small, the items that begin in an equal range, so that no item is shared with
+  // another block (arriving and joining cost 3 us, a small item more than the others' 1 us)
   const int64_t total = (int64_t)before[B] * pl.items;
-  const int64_t share = paged_share(total, pl.workers, pl.per_worker);
-  const int64_t u0 = w * share, u1 = min(total, u0 + share);
+  int64_t range, share, a0, a1;
+  if (most <= S::WHOLE) {
+    range = paged_share(total, gridDim.x, pl.per_block);
+    for (int i = warp; i < 2; i += pl.warps) {
+      const int64_t edge = pat_item_start(before, B, pl, min(total, (blockIdx.x + i) * range), total);
+      if (lane == 0) s_edge[i] = edge;
+    }
+    __syncthreads();
+    a0 = s_edge[0];
+    a1 = s_edge[1];
+    share = max((int)(a1 - a0 + pl.warps - 1) / pl.warps, 1);
+  } else {
+    share = paged_share(total, pl.workers, pl.per_worker);
+    range = share * pl.warps;
+    a0 = min(total, blockIdx.x * range);
+    a1 = min(total, a0 + range);
+  }
+  if (a0 >= a1) return;  // a block without work
+  const int64_t u0 = a0 + warp * share, u1 = min(a1, u0 + share);
   if (u0 < u1) {
     const int64_t n = u1 - u0;
     // copies: tile `pc`; the pages of its keys have been read a tile ahead (BOX: the one page, by
@@ -840,7 +880,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
     PagedCursor pc = pat_locate(before, B, pl, u0);
     const PagedCursor first = pc;
     if (threadIdx.x == 0 && first.tile > 0) {
-      word[1] = pl.arrived + (int)paged_div(u0 - first.tile, share) / pl.warps;
+      word[1] = pl.arrived + (int)paged_div(u0 - first.tile, range);
       seen_word[1] = pat_look(word[1]);
     }
     const int cap = a.c.max_pages << a.c.log2_page, slots = (1 << a.c.log2_page) - 1;
@@ -982,11 +1022,14 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
         out.hd = HD;
         pw.finish(lane, out);
         if (!whole && lane == 0 && (from == 0 || warp == 0)) {
-          const int64_t start = u0 + t - c.tile;  // the item's first tile
-          const int k = from == 0 ? warp + 1 : 0, w0 = from == 0 ? w : (int)paged_div(start, share);
-          const int w1 = (int)paged_div(start + c.tiles - 1, share);
-          s_split[k] = Split{c.seq, h, out.rows, w0 / pl.warps, w1 / pl.warps, max(w0 - wb, 0), min(w1, we) - wb};
-          if (k == 0 || w1 > we) s_cross[k > 0] = k;
+          const int64_t start = u0 + t - c.tile, last = start + c.tiles - 1;  // the item's first and last tile
+          const int k = from == 0 ? warp + 1 : 0;
+          Split sp{c.seq, h, out.rows, (int)blockIdx.x, (int)blockIdx.x, from == 0 ? warp : 0, pl.warps - 1};
+          if (last < a1) sp.p1 = (int)paged_div(last - a0, share);
+          if (k == 0) sp.b0 = (int)paged_div(start, range);
+          if (last >= a1) sp.b1 = (int)paged_div(last, range);
+          s_split[k] = sp;
+          if (k == 0 || last >= a1) s_cross[k > 0] = k;
         }
       }
       if (t + 1 < n) paged_next(c, before, pl.items);
@@ -998,7 +1041,6 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
     if (!BOX) cp_async_wait<0>();
     if (bad) raise_device_error(a.c.status, bad == 2 ? DEV_TIMEOUT : DEV_PAGE_RANGE);
   }
-  if ((int64_t)wb * share >= total) return;  // a block without work
   __syncthreads();
   // a thread joins four elements of a split item's row over the block's pieces
   constexpr int VEC = HD / 4;
