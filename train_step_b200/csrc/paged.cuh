@@ -200,14 +200,14 @@ struct PagedAttnArgs {
 // rectangle of a page and arrives by tensor copies that one lane issues; smaller pages, and
 // strides that a tensor map does not take, go through 16-byte copies by all lanes.
 // What bounds it. Long caches: reading them from HBM; 128 sequences of 512 to 8,192 tokens with 8
-// key heads of 128 (1.46 GB) take 238 us, 6.1 TB/s, where a kernel that only reads as many random
-// pages in equal shares reaches 6.6 TB/s. Before that it was the instructions of a warp: two or
-// three warps per scheduler, each a chain of dependent steps, of which 16-byte copies by all
-// lanes were half (300 us). Short ones: the chain of lengths, place, page, copy, first tile
-// (4 us) and, when items cross blocks, arrival and join (4 us): 16 sequences of 1,024 tokens, 12
-// heads of 64 (50 MB) take 17.6 us, of which 7 us stream.
-// Pages that keep each head's tokens together read faster than pages of whole tokens (25 heads
-// of 64: 95 % and 77 % of the copy rate), whose rows of 128 bytes are far apart.
+// key heads of 128 (1.46 GB) take 225 us, 6.5 TB/s, as fast as a plain copy moves bytes. Before
+// that it was the instructions of a warp: two or three warps per scheduler, each a chain of
+// dependent steps, of which 16-byte copies by all lanes were half (300 us). Shorter ones: the
+// chain of lengths, place, page, copy, first tile (3.5 us) and, when items cross blocks, arrival
+// and join (3 to 4 us): 16 sequences of 1,024 tokens, 12 heads of 64 (50 MB) take 16.3 us, of
+// which 7 us stream; one of 100 tokens 5.4 us.
+// Pages that keep each head's tokens together read faster than pages of whole tokens, whose rows
+// of 128 bytes are far apart (12 and 25 heads of 64: 94 % against 85 and 77 % of the copy rate).
 constexpr int PAT_MAX_BLOCKS = 256;
 constexpr int PAT_SMEM = 226 * 1024;  // of a block
 
@@ -221,7 +221,7 @@ struct PatShape {
   static constexpr int BOXES = (ROW + BOX_ROW - 1) / BOX_ROW;
   static constexpr int BOX = PAT_TILE * BOX_ROW;
   static constexpr int TILE = BOXES * BOX;
-  static constexpr int STAGES = 2;  // more of them cost warps, and were slower
+  static constexpr int STAGES = 2;  // 3: 224 -> 244 us on the 1.46 GB above, with as many warps
   // fp32: a copy of the item's queries and the tile's weights, per warp
   static constexpr int SIDE = sizeof(T) == 4 ? QR * ROW + QR * PAT_TILE * 4 : 0;
   // a piece: outputs, then (maximum, sum), of each row; a warp: its ring of keys and values

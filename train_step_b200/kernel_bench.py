@@ -4,6 +4,8 @@
     python -m train_step_b200.kernel_bench attn --B 16 --T 1024 --H 12
     python -m train_step_b200.kernel_bench ln --N 16384 --C 768
     python -m train_step_b200.kernel_bench decode --B 16 --T0 512 --steps 64
+    python -m train_step_b200.kernel_bench paged_attn --B 32 --T 4096 --H 32 --KV 8 --hd 128
+    python -m train_step_b200.kernel_bench paged_append --B 16 --T 1024 --H 12 --KV 12 --hd 64
 
 Used for focused profiler captures of one kernel on a small case. Inputs are
 seeded random tensors; nothing is checked here (the tests check numerics).
@@ -69,6 +71,37 @@ def gemv_bench(a) -> dict:
     return dict(B=a.B, gemv=out)
 
 
+def paged_bench(a) -> dict:
+    """The paged cache's calls on B sequences of T tokens (bf16, pages of a.page tokens, each
+    head's tokens together, pages in random order): the attention of one new token each, or the
+    append of all B*T tokens with the rotation of keys and queries. Bytes: every key and value
+    (and query and output) once."""
+    B, T, H, KV, hd, P = a.B, a.T, a.H, a.KV, a.hd, a.page
+    per = (T + P - 1) // P
+    table = torch.randperm(B * per, device="cuda").view(B, per).to(torch.int32)
+    kc, vc = (torch.randn(B * per, KV, P, hd, device="cuda", dtype=torch.bfloat16).transpose(1, 2) for _ in range(2))
+    kv = tsb.PagedKV(kc, vc, table)
+    if a.kernel == "paged_attn":
+        q = torch.randn(B, H, hd, device="cuda", dtype=torch.bfloat16)
+        out, ws = torch.empty_like(q), kv.attention_workspace(H)
+        lens = torch.full((B,), T, device="cuda", dtype=torch.int32)
+        ms = timeit(lambda: tsb.paged_attention(kv, q, lens, out, ws=ws), a.iters)
+        by = 4.0 * B * T * KV * hd + 4.0 * B * H * hd
+    else:
+        qkv = torch.randn(B * T, H + 2 * KV, hd, device="cuda", dtype=torch.bfloat16)
+        q, k, v = qkv.split([H, KV, KV], 1)
+        q_out = torch.empty(B * T, H, hd, device="cuda", dtype=torch.bfloat16)
+        pos = torch.arange(T, device="cuda", dtype=torch.int32).repeat(B)
+        seq = torch.arange(B, device="cuda", dtype=torch.int32).repeat_interleave(T)
+        cs = tsb.rotation_table(T, hd)
+        ms = timeit(lambda: tsb.paged_kv_append(kv, k, v, pos, seq, q=q, q_out=q_out, cos_sin=cs), a.iters)
+        by = 4.0 * B * T * (H + 2 * KV) * hd + 4.0 * T * hd
+    kv.check()
+    peak, which = hbm_peak()
+    gbs = by / (ms * 1e-3) / 1e9
+    return dict(shape=[B, T, H, KV, hd, P], ms=ms, bytes=by, gbs=gbs, of_hbm=gbs / peak, peak=which)
+
+
 def decode_bench(a) -> dict:
     """Generation with the key/value cache on GPT-2 124M (random weights): B prompts of T0
     tokens, then `steps` decode steps, each one forward step for all B sequences followed
@@ -127,7 +160,8 @@ def decode_bench(a) -> dict:
 
 def main() -> None:
     ap = argparse.ArgumentParser()
-    ap.add_argument("kernel", choices=["gemm", "attn", "attn_bwd", "ln", "ln_bwd", "ce", "decode", "gemv"])
+    ap.add_argument("kernel", choices=["gemm", "attn", "attn_bwd", "ln", "ln_bwd", "ce", "decode", "gemv",
+                                       "paged_attn", "paged_append"])
     ap.add_argument("--M", type=int, default=16384)
     ap.add_argument("--N", type=int, default=3072)
     ap.add_argument("--K", type=int, default=768)
@@ -145,6 +179,9 @@ def main() -> None:
     ap.add_argument("--iters", type=int, default=20)
     ap.add_argument("--stored", action="store_true", help="attn_bwd: the training step's stored-dS form")
     ap.add_argument("--T0", type=int, default=512, help="decode: prompt length")
+    ap.add_argument("--KV", type=int, default=12, help="paged: key heads")
+    ap.add_argument("--hd", type=int, default=64, help="paged: head size")
+    ap.add_argument("--page", type=int, default=16, help="paged: tokens of a page")
     ap.add_argument("--steps", type=int, default=64, help="decode: generated tokens per sequence")
     ap.add_argument("--topk", type=int, default=50, help="decode: k of the sampler")
     a = ap.parse_args()
@@ -220,6 +257,8 @@ def main() -> None:
         res.update(decode_bench(a))
     elif a.kernel == "gemv":
         res.update(gemv_bench(a))
+    elif a.kernel in ("paged_attn", "paged_append"):
+        res.update(paged_bench(a))
     else:
         N, V = a.M, a.V
         ld = (V + 63) // 64 * 64
