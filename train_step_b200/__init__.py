@@ -637,6 +637,7 @@ class PagedKV:
         # looked up once: a call takes a few microseconds
         self._append, self._attention = lib().gpt2_op_paged_kv_append, lib().gpt2_op_paged_attention
         self._index, self._scale = k_cache.get_device(), self.head_dim ** -0.5
+        self._inner = (self.head_dim, 1)  # strides of a head and of an element in a row
         self._int32, self._float32 = torch.int32, torch.float32
         self._current_device, self._current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
@@ -649,23 +650,33 @@ class PagedKV:
     def check(self, stream=None) -> None:
         """Wait for the stream and raise Gpt2Error(GPT2_ERR_PAGE_RANGE) if a call on this cache
         met a bad page id, sequence, position or length since the last check."""
-        self._call(lib().gpt2_op_paged_status, (), stream)
+        self._call(lib().gpt2_op_paged_status, stream=stream)
 
-    def _rows(self, name, t, rows, heads):
-        """[rows, heads, head_dim] of the cache's type and device, heads contiguous: the row stride."""
+    def _ld(self, name, t, rows, heads):
+        """The row stride of t, which must be [rows, heads, head_dim] of the cache's type and
+        device with the heads of a row contiguous."""
         st = t.stride()
-        if (t.shape != (rows, heads, self.head_dim) or t.dtype is not self.dtype
-                or t.get_device() != self._index or st[2] != 1 or (st[1] != self.head_dim and heads > 1)):
+        if (t.shape != (rows, heads, self.head_dim) or t.dtype is not self.dtype or t.get_device() != self._index
+                or (st[1:] != self._inner and (heads > 1 or st[2] != 1))):
             raise ValueError(f"{name} must be [{rows}, {heads}, {self.head_dim}] {self.dtype} on {self.device}, "
                              "with the heads of a row contiguous")
         return st[0] if rows > 1 else heads * self.head_dim
 
     def _ints(self, name, t, n):
-        if (t.dtype is not self._int32 or t.shape != (n,) or t.get_device() != self._index or not t.is_contiguous()):
+        """The address of t, which must be a contiguous int32 vector of n on the cache's device."""
+        if (t.dtype is not self._int32 or t.shape != (n,) or t.get_device() != self._index
+                or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {self.device}")
         return t.data_ptr()
 
-    def _call(self, f, args, stream) -> None:
+    def _floats(self, name, t, shape):
+        """The address of t, which must be a contiguous fp32 tensor of that shape on the device."""
+        if (t.dtype is not self._float32 or t.shape != shape or t.get_device() != self._index
+                or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous fp32 tensor {list(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def _call(self, f, *args, stream=None) -> None:
         """f(cache, *args, stream) with the cache's device current; torch's current stream of that
         device by default."""
         if self._current_device() == self._index:
@@ -684,26 +695,22 @@ def paged_kv_append(cache: PagedKV, k, v, positions, seqs=None, q=None, q_out=No
     positions[n] (int32; negative: a padding row) of sequence seqs[n] (int32; None: n). With
     cos_sin (fp32 [n_positions, rot_dim], see rotation_table) keys are rotated on the way, and
     q [N, n_heads, head_dim] is rotated into q_out (may be q). See gpt2_op_paged_kv_append."""
-    N = k.shape[0]
-    ldk, ldv = cache._rows("k", k, N, cache.n_kv_heads), cache._rows("v", v, N, cache.n_kv_heads)
-    pos = cache._ints("positions", positions, N)
-    seq = None if seqs is None else cache._ints("seqs", seqs, N)
+    N, KV = k.shape[0], cache.n_kv_heads
+    ldk, ldv = cache._ld("k", k, N, KV), cache._ld("v", v, N, KV)
     nh = ldq = ldqo = n_pos = rot = 0
     pq = pqo = pcs = None
     if q is not None and q_out is not None:
         nh = q.shape[1] if q.dim() == 3 else 1
-        ldq, ldqo = cache._rows("q", q, N, nh), cache._rows("q_out", q_out, N, nh)
+        ldq, ldqo = cache._ld("q", q, N, nh), cache._ld("q_out", q_out, N, nh)
         pq, pqo = q.data_ptr(), q_out.data_ptr()
     elif q is not q_out:
         raise ValueError("q and q_out go together")
     if cos_sin is not None:
-        if (cos_sin.dim() != 2 or cos_sin.dtype is not cache._float32 or cos_sin.get_device() != cache._index
-                or not cos_sin.is_contiguous()):
-            raise ValueError(f"cos_sin must be a contiguous fp32 tensor [n_positions, rot_dim] on {cache.device}")
+        pcs = cache._floats("cos_sin", cos_sin, cos_sin.shape if cos_sin.dim() == 2 else ("n_positions", "rot_dim"))
         n_pos, rot = cos_sin.shape
-        pcs = cos_sin.data_ptr()
-    cache._call(cache._append, (k.data_ptr(), ldk, v.data_ptr(), ldv, pq, ldq, pqo, ldqo, nh, N, pos, seq, pcs, n_pos,
-                                rot, int(interleaved)), stream)
+    cache._call(cache._append, k.data_ptr(), ldk, v.data_ptr(), ldv, pq, ldq, pqo, ldqo, nh, N,
+                cache._ints("positions", positions, N), None if seqs is None else cache._ints("seqs", seqs, N), pcs,
+                n_pos, rot, int(interleaved), stream=stream)
 
 
 def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None, window: int = 0, sinks: int = 0,
@@ -715,14 +722,7 @@ def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None
     (None: allocated for this one). See gpt2_op_paged_attention."""
     B = cache.n_seqs
     nh = q.shape[1] if q.dim() == 3 else 1
-    ldq, ldo = cache._rows("q", q, B, nh), cache._rows("out", out, B, nh)
-    lens = cache._ints("seq_lens", seq_lens, B)
-    pl = None
-    if lse is not None:
-        if (lse.dtype is not cache._float32 or lse.shape != (B, nh) or lse.get_device() != cache._index
-                or not lse.is_contiguous()):
-            raise ValueError(f"lse must be a contiguous fp32 tensor [{B}, {nh}] on {cache.device}")
-        pl = lse.data_ptr()
+    ldq, ldo = cache._ld("q", q, B, nh), cache._ld("out", out, B, nh)
     if not (0 <= window < 2 ** 31 and 0 <= sinks < 2 ** 31):
         raise ValueError("window and sinks must be in [0, 2^31)")
     if ws is None:
@@ -731,8 +731,9 @@ def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None
         ws = cache.attention_workspace(nh)
     elif ws.get_device() != cache._index or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {cache.device}")
-    cache._call(cache._attention, (q.data_ptr(), ldq, nh, lens, cache._scale if scale is None else scale, window, sinks,
-                                   out.data_ptr(), ldo, pl, ws.data_ptr(), ws.nbytes), stream)
+    cache._call(cache._attention, q.data_ptr(), ldq, nh, cache._ints("seq_lens", seq_lens, B),
+                cache._scale if scale is None else scale, window, sinks, out.data_ptr(), ldo,
+                None if lse is None else cache._floats("lse", lse, (B, nh)), ws.data_ptr(), ws.nbytes, stream=stream)
 
 
 def rotation_table(n_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):
