@@ -620,6 +620,47 @@ def test_captured_step_replays_with_new_lengths(dtype):
     kv.check()
 
 
+def test_captured_behind_copies_and_other_streams():
+    # the calls start early behind other kernels; here copies, fills and a joined stream precede
+    kv, q, ln, out, lse, _ = attention_case([3000, 10, 700], 8, 2, 64, 16, torch.bfloat16, "heads", seed=23)
+    ws, got, n, qq = kv.attention_workspace(8), torch.empty_like(out), torch.zeros_like(ln), torch.zeros_like(q)
+    k, v = torch.randn(2, 3, 2, 64).bfloat16().cuda().unbind(0)
+    pos = torch.empty_like(ln)
+    side = torch.cuda.Stream()
+    before = kv.k_cache.clone(), kv.v_cache.clone()
+    torch.cuda.synchronize()
+
+    def body():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            qq.copy_(q)
+        n.copy_(ln)
+        got.zero_()
+        torch.sub(ln, 1, out=pos)
+        torch.cuda.current_stream().wait_stream(side)
+        tsb.paged_kv_append(kv, k, v, pos)
+        tsb.paged_attention(kv, qq, n, got, ws=ws)
+        kv.k_cache.copy_(before[0])  # as it was, for the next run
+        kv.v_cache.copy_(before[1])
+
+    body()
+    torch.cuda.synchronize()
+    want = got.clone()
+    assert not torch.equal(want, out)  # the appended tokens count
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        body()
+    for _ in range(20):
+        for t in (qq, n, pos, got):
+            t.zero_()
+        gr.replay()
+        assert torch.equal(got, want)
+    for _ in range(20):
+        body()
+        assert torch.equal(got, want)
+    kv.check()
+
+
 def test_captured_calls_share_a_workspace_in_turn():
     kv, q, ln, out, lse, _ = attention_case([3000, 10, 700], 8, 2, 64, 16, torch.bfloat16, "heads", seed=22)
     ws = kv.attention_workspace(8)

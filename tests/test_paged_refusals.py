@@ -107,7 +107,8 @@ def test_attention_of_no_sequences_does_nothing():
 def test_workspace_size():
     f = tsb.lib().gpt2_paged_attention_ws_bytes
     assert f(3, 4, 2, 64) > 0 and f(0, 4, 2, 64) > 0 and f(4096, 128, 1, 128) > 0
-    for bad in ((-1, 4, 2, 64), (4097, 4, 2, 64), (3, 5, 2, 64), (3, 0, 2, 64), (3, 4, 0, 64), (3, 4, 2, 0)):
+    for bad in ((-1, 4, 2, 64), (4097, 4, 2, 64), (3, 5, 2, 64), (3, 0, 2, 64), (3, 4, 0, 64), (3, 4, 2, 0),
+                (3, 4, 2, 48)):
         assert f(*bad) == 0
 
 

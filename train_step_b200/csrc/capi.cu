@@ -31,6 +31,16 @@ struct LayerP {
 
 thread_local std::string g_op_error;
 
+// f(), with no exception (host memory that ran out) across the C boundary
+template <class F>
+int guarded(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return GPT2_ERR_OOM;
+  }
+}
+
 uint64_t splitmix64_at(uint64_t x) {
   uint64_t z = x + 0x9E3779B97F4A7C15ull;
   z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
@@ -1551,7 +1561,7 @@ int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const void* k, int64_t ldk,
   a.cos_sin = cos_sin;
   a.n_positions = n_positions;
   a.rot = rot_dim;
-  return paged_kv_append(o.c, kv, a, interleaved != 0);
+  return guarded([&] { return paged_kv_append(o.c, kv, a, interleaved != 0); });
 }
 
 size_t gpt2_paged_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim) {
@@ -1573,7 +1583,7 @@ int gpt2_op_paged_attention(const gpt2_paged_kv* kv, const void* q, int64_t ldq,
   a.scale = scale;
   a.window = window;
   a.sinks = sinks;
-  return paged_attention(o.c, kv, a, ws, ws_bytes);
+  return guarded([&] { return paged_attention(o.c, kv, a, ws, ws_bytes); });
 }
 
 int gpt2_op_paged_status(const gpt2_paged_kv* kv, void* stream) {

@@ -1142,6 +1142,7 @@ inline int sample_topk(const LaunchCtx& c, const float* logits, int64_t ld, int 
 // paged key/value cache
 // ---------------------------------------------------------------------------
 constexpr int PAGED_MAX_SEQS = 4096;
+inline bool paged_head_dim_ok(int hd) { return hd == 32 || hd == 64 || hd == 96 || hd == 128; }
 
 // Checks a caller's cache description and fills the kernels' view of it.
 inline int paged_view(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedView* out) {
@@ -1149,7 +1150,7 @@ inline int paged_view(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedView* ou
     return fail(c, GPT2_ERR_CONFIG, "paged cache: k, v and page_table are required");
   if (kv->dtype != GPT2_BF16 && kv->dtype != GPT2_FP32)
     return fail(c, GPT2_ERR_CONFIG, "paged cache: dtype must be GPT2_FP32 or GPT2_BF16");
-  if (kv->head_dim != 32 && kv->head_dim != 64 && kv->head_dim != 96 && kv->head_dim != 128)
+  if (!paged_head_dim_ok(kv->head_dim))
     return fail(c, GPT2_ERR_CONFIG, "paged cache: head_dim must be 32, 64, 96 or 128");
   if (kv->n_pages < 1 || kv->max_pages < 1 || kv->n_kv_heads < 1 || kv->n_seqs < 0 || kv->table_stride < kv->max_pages)
     return fail(c, GPT2_ERR_CONFIG,
@@ -1225,7 +1226,7 @@ inline bool paged_heads_ok(int nh, int nkv) { return nkv >= 1 && nh >= 1 && nh <
 // Partial results of at most PAT_MAX_BLOCKS blocks: two each, of min(16, group) rows; and an
 // arrival word each.
 inline size_t paged_attention_ws_bytes(int n_seqs, int nh, int nkv, int hd) {
-  if (n_seqs < 0 || n_seqs > PAGED_MAX_SEQS || !paged_heads_ok(nh, nkv) || hd < 1 || hd > 128) return 0;
+  if (n_seqs < 0 || n_seqs > PAGED_MAX_SEQS || !paged_heads_ok(nh, nkv) || !paged_head_dim_ok(hd)) return 0;
   const size_t rows = std::min(16, nh / nkv);
   return (size_t)PAT_MAX_BLOCKS * (8 + 2 * rows * (8 + (size_t)hd * 4));
 }

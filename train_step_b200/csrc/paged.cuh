@@ -891,7 +891,8 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       pos = paged_tile_pos(vis, pc.tile);
       const int mine = BOX ? pos : pos + lane;
       if (BOX || (lane < PAT_TILE && mine < vis.len))
-        page = a.c.table[pc.seq * a.c.table_stride + (mine >> a.c.log2_page)];
+        // (the bound: a length that changes during the call must not lead out of the table)
+        page = a.c.table[pc.seq * a.c.table_stride + min(mine >> a.c.log2_page, a.c.max_pages - 1)];
     };
     auto copy_tile = [&](int stage, bool with_q) {
       const uint32_t seen = paged_tile_mask(vis, pos);
