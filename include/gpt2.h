@@ -454,24 +454,30 @@ typedef struct {
   int32_t dtype, n_pages, page_size, max_pages, n_seqs, n_kv_heads, head_dim;
 } gpt2_paged_kv;
 
-/* Append the keys and values of N new tokens. Row n (n_kv_heads heads of head_dim contiguous
- * elements at k + n*ldk and v + n*ldv) goes to position positions[n] of sequence seqs[n]
- * (seqs NULL: sequence n, N <= n_seqs). positions[n] < 0 marks a padding row: it is skipped.
- * With rot_dim > 0 (a multiple of 16, at most head_dim) the keys are rotated on the way by
- * the table f32_cos_sin [n_positions][rot_dim] (16-byte aligned; row t: the rot_dim/2 cosines,
+/* Append the keys and values of n_rows new tokens. Row n (n_kv_heads heads of head_dim
+ * contiguous elements at k + n*ldk and v + n*ldv) goes to position positions[n] of sequence
+ * seqs[n] (seqs NULL: sequence n, n_rows <= n_seqs). positions[n] < 0 marks a padding row: it is
+ * skipped. With rot_dim > 0 (a multiple of 16, at most head_dim) the keys are rotated on the way
+ * by the table f32_cos_sin [n_positions][rot_dim] (16-byte aligned; row t: the rot_dim/2 cosines,
  * then the sines, of position t): the pair (x, y) of elements (i, i + rot_dim/2), or (2i,
  * 2i + 1) when interleaved != 0, becomes (x c_i - y s_i, x s_i + y c_i), computed in fp32 and
- * rounded once; elements from rot_dim on are copied. N times the vectors of a row is limited
- * (GPT2_ERR_BATCH): N * (n_q_heads + 2 n_kv_heads) * head_dim elements of at most 32 GB. q (nullable, with q_out and n_q_heads):
+ * rounded once; elements from rot_dim on are copied. q (nullable, with q_out and n_q_heads):
  * query rows of the same tokens, rotated the same way into q_out (may be q itself, with the
- * same row stride). A row whose position, sequence, table entry or rotation row is outside
- * its range is skipped and raises the status word; rows that are skipped leave q_out as it
- * was. Rows must name distinct slots: of two rows for one slot, each 16 bytes come from
- * either. Row bases and strides are multiples of 16 bytes. */
-int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const void* k, int64_t ldk, const void* v, int64_t ldv,
-                            const void* q, int64_t ldq, void* q_out, int64_t ldqo, int n_q_heads, int N,
-                            const int32_t* positions, const int32_t* seqs, const float* f32_cos_sin, int n_positions,
-                            int rot_dim, int interleaved, void* stream);
+ * same row stride, but not overlap it otherwise). A row whose position, sequence, table entry or
+ * rotation row is outside its range is skipped and raises the status word; rows that are skipped
+ * leave q_out as it was. Rows must name distinct slots: of two rows for one slot, each 16 bytes
+ * come from either. Row bases and strides (elements) are multiples of 16 bytes; n_rows *
+ * (n_q_heads + 2 n_kv_heads) * head_dim elements are at most 32 GB (GPT2_ERR_BATCH). The struct
+ * is read during the call only. */
+typedef struct {
+  const void *k, *v, *q;
+  void* q_out;
+  int64_t ldk, ldv, ldq, ldqo;
+  const int32_t *positions, *seqs;
+  const float* f32_cos_sin;
+  int32_t n_rows, n_q_heads, n_positions, rot_dim, interleaved;
+} gpt2_paged_rows;
+int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const gpt2_paged_rows* rows, void* stream);
 
 /* Attention of one new token per sequence over the cache: for each sequence b with L =
  * seq_lens[b] cached tokens (the new one, already appended, is the last) and each query head
@@ -484,12 +490,22 @@ int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const void* k, int64_t ldk,
  * the nearer end, a key whose page id is bad is left out, and both raise the status word.
  * Softmax statistics and sums are fp32, each output is rounded once; a NaN in q, or in a
  * visible key or value, gives NaN where the formula does, one in an unseen place has no effect.
- * 0 < scale <= 1e38. out may not overlap q, the cache or ws. ws: DEVICE workspace of gpt2_paged_attention_ws_bytes bytes, 16-byte
- * aligned, of any content; calls that may run at the same time need one each.
- * Deterministic for given lengths. */
-int gpt2_op_paged_attention(const gpt2_paged_kv* kv, const void* q, int64_t ldq, int n_q_heads,
-                            const int32_t* seq_lens, float scale, int window, int sinks, void* out, int64_t ldo,
-                            float* f32_lse, void* ws, size_t ws_bytes, void* stream);
+ * 0 < scale <= 1e38. out may not overlap q, the cache or ws. ws: DEVICE workspace of
+ * gpt2_paged_attention_ws_bytes bytes, 16-byte aligned, of any content; calls that may run at
+ * the same time need one each. Deterministic for given lengths. The struct is read during the
+ * call only. */
+typedef struct {
+  const void* q;
+  void* out;
+  float* f32_lse;
+  const int32_t* seq_lens;
+  void* ws;
+  size_t ws_bytes;
+  int64_t ldq, ldo;
+  int32_t n_q_heads, window, sinks;
+  float scale;
+} gpt2_paged_query;
+int gpt2_op_paged_attention(const gpt2_paged_kv* kv, const gpt2_paged_query* query, void* stream);
 
 /* Bytes of gpt2_op_paged_attention's workspace (0 for sizes it refuses). */
 size_t gpt2_paged_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim);

@@ -2,6 +2,8 @@
 index arithmetic they share with the kernels is checked exhaustively (CPU only)."""
 import ctypes as ct
 import os
+import re
+import struct
 import subprocess
 
 import pytest
@@ -31,17 +33,18 @@ def append(kv, **kw):
     f = dict(k=A, ldk=128, v=A, ldv=128, q=A, ldq=256, q_out=A, ldqo=256, nh=4, N=3, positions=A, seqs=A, cos_sin=A,
              n_positions=128, rot=64, pairs=0)
     f.update(kw)
-    return tsb.lib().gpt2_op_paged_kv_append(kv if kv is None else ct.byref(kv), f["k"], f["ldk"], f["v"], f["ldv"],
-                                             f["q"], f["ldq"], f["q_out"], f["ldqo"], f["nh"], f["N"], f["positions"],
-                                             f["seqs"], f["cos_sin"], f["n_positions"], f["rot"], f["pairs"], None)
+    rows = tsb._PAGED_ROWS.pack(*(f[n] or 0 for n in (
+        "k", "v", "q", "q_out", "ldk", "ldv", "ldq", "ldqo", "positions", "seqs", "cos_sin", "N", "nh", "n_positions",
+        "rot", "pairs")))
+    return tsb.lib().gpt2_op_paged_kv_append(kv if kv is None else ct.byref(kv), rows, None)
 
 
 def attend(kv, **kw):
     f = dict(q=A, ldq=256, nh=4, lens=A, scale=0.125, window=0, sinks=0, out=A, ldo=256, lse=A, ws=A, ws_bytes=1 << 40)
     f.update(kw)
-    return tsb.lib().gpt2_op_paged_attention(kv if kv is None else ct.byref(kv), f["q"], f["ldq"], f["nh"], f["lens"],
-                                             f["scale"], f["window"], f["sinks"], f["out"], f["ldo"], f["lse"],
-                                             f["ws"], f["ws_bytes"], None)
+    query = tsb._PAGED_QUERY.pack(*(f[n] or 0 for n in (
+        "q", "out", "lse", "lens", "ws", "ws_bytes", "ldq", "ldo", "nh", "window", "sinks", "scale")))
+    return tsb.lib().gpt2_op_paged_attention(kv if kv is None else ct.byref(kv), query, None)
 
 
 BAD_CACHES = [
@@ -66,6 +69,9 @@ def test_a_bad_cache_is_refused_by_both_calls(change, code):
 
 def test_a_null_cache_is_refused():
     assert append(None) == CONFIG and attend(None) == CONFIG
+    kv = cache()
+    assert tsb.lib().gpt2_op_paged_kv_append(ct.byref(kv), None, None) == CONFIG
+    assert tsb.lib().gpt2_op_paged_attention(ct.byref(kv), None, None) == CONFIG
     assert tsb.lib().gpt2_op_paged_status(None, None) == CONFIG
     assert tsb.lib().gpt2_op_paged_status(ct.byref(cache()), None) == CONFIG  # no status word
 
@@ -110,6 +116,25 @@ def test_workspace_size():
     for bad in ((-1, 4, 2, 64), (4097, 4, 2, 64), (3, 5, 2, 64), (3, 0, 2, 64), (3, 4, 0, 64), (3, 4, 2, 0),
                 (3, 4, 2, 48)):
         assert f(*bad) == 0
+
+
+def test_packed_structs_are_those_of_the_header(tmp_path):
+    src = tmp_path / "layout.c"
+    names = ["k", "v", "q", "q_out", "ldk", "ldv", "ldq", "ldqo", "positions", "seqs", "f32_cos_sin", "n_rows",
+             "n_q_heads", "n_positions", "rot_dim", "interleaved"]
+    query = ["q", "out", "f32_lse", "seq_lens", "ws", "ws_bytes", "ldq", "ldo", "n_q_heads", "window", "sinks", "scale"]
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "gpt2.h"\nint main(void) {\n' + "".join(
+        f'printf("%zu ", offsetof({t}, {n}));\n' for t, ns in (("gpt2_paged_rows", names), ("gpt2_paged_query", query),
+        ("gpt2_paged_kv", [f[0] for f in tsb._PagedKV._fields_])) for n in ns) + "return 0; }\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I" + os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+
+    def offsets(fmt):
+        codes = "".join(c * int(n or 1) for n, c in re.findall(r"(\d*)([a-zA-Z])", fmt))
+        return [struct.calcsize("@" + codes[:i] + "0" + codes[i]) for i in range(len(codes))]
+    assert got == (offsets(tsb._PAGED_ROWS.format) + offsets(tsb._PAGED_QUERY.format)
+                   + [getattr(tsb._PagedKV, f[0]).offset for f in tsb._PagedKV._fields_])
 
 
 INDEX_CHECK = r"""

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as ct
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -40,6 +41,11 @@ class _PagedKV(ct.Structure):
                 ("head_stride", ct.c_int64), ("page_table", ct.c_void_p), ("table_stride", ct.c_int64),
                 ("status", ct.c_void_p)] + [(n, ct.c_int32) for n in (
                     "dtype", "n_pages", "page_size", "max_pages", "n_seqs", "n_kv_heads", "head_dim")]
+
+
+# gpt2_paged_rows and gpt2_paged_query, as bytes: one packing costs less than 16 converted arguments
+_PAGED_ROWS = struct.Struct("@4P4q3P5i")
+_PAGED_QUERY = struct.Struct("@5PN2q3if")
 
 
 _lib = None
@@ -115,12 +121,8 @@ _SYMBOLS = {
                              ct.POINTER(ct.c_int64), ct.POINTER(ct.c_int), ct.POINTER(ct.c_int64)], ct.c_int),
     "gpt2_set_grad_events": ([ct.c_void_p, ct.POINTER(ct.c_void_p), ct.c_int], ct.c_int),
     "gpt2_read_loss": ([ct.c_void_p, ct.POINTER(ct.c_float)], ct.c_int),
-    "gpt2_op_paged_kv_append": ([ct.POINTER(_PagedKV), ct.c_void_p, ct.c_int64, ct.c_void_p, ct.c_int64, ct.c_void_p,
-                                 ct.c_int64, ct.c_void_p, ct.c_int64, ct.c_int, ct.c_int, ct.c_void_p, ct.c_void_p,
-                                 ct.c_void_p, ct.c_int, ct.c_int, ct.c_int, ct.c_void_p], ct.c_int),
-    "gpt2_op_paged_attention": ([ct.POINTER(_PagedKV), ct.c_void_p, ct.c_int64, ct.c_int, ct.c_void_p, ct.c_float,
-                                 ct.c_int, ct.c_int, ct.c_void_p, ct.c_int64, ct.c_void_p, ct.c_void_p, ct.c_size_t,
-                                 ct.c_void_p], ct.c_int),
+    "gpt2_op_paged_kv_append": ([ct.POINTER(_PagedKV), ct.c_char_p, ct.c_void_p], ct.c_int),
+    "gpt2_op_paged_attention": ([ct.POINTER(_PagedKV), ct.c_char_p, ct.c_void_p], ct.c_int),
     "gpt2_paged_attention_ws_bytes": ([ct.c_int, ct.c_int, ct.c_int, ct.c_int], ct.c_size_t),
     "gpt2_op_paged_status": ([ct.POINTER(_PagedKV), ct.c_void_p], ct.c_int),
     "gpt2_op_last_error": ([], ct.c_char_p),
@@ -597,6 +599,11 @@ def cross_entropy(logits, V, targets, scale, row_loss, stream=None):
                                     _stream(stream)))
 
 
+def _device_of(index):
+    import torch
+    return torch.cuda.device(index)
+
+
 class PagedKV:
     """A paged key/value cache on caller-owned CUDA tensors (see gpt2_paged_kv).
 
@@ -650,7 +657,8 @@ class PagedKV:
     def check(self, stream=None) -> None:
         """Wait for the stream and raise Gpt2Error(GPT2_ERR_PAGE_RANGE) if a call on this cache
         met a bad page id, sequence, position or length since the last check."""
-        self._call(lib().gpt2_op_paged_status, stream=stream)
+        with _device_of(self._index):
+            _op(lib().gpt2_op_paged_status(self._ref, self._current_stream(self._index) if stream is None else stream))
 
     def _ld(self, name, t, rows, heads):
         """The row stride of t, which must be [rows, heads, head_dim] of the cache's type and
@@ -676,15 +684,17 @@ class PagedKV:
             raise ValueError(f"{name} must be a contiguous fp32 tensor {list(shape)} on {self.device}")
         return t.data_ptr()
 
-    def _call(self, f, *args, stream=None) -> None:
-        """f(cache, *args, stream) with the cache's device current; torch's current stream of that
+    def _call(self, f, args, stream) -> None:
+        """f(cache, args, stream) with the cache's device current; torch's current stream of that
         device by default."""
+        if stream is None:
+            stream = self._current_stream(self._index)
         if self._current_device() == self._index:
-            rc = f(self._ref, *args, self._current_stream(self._index) if stream is None else stream)
+            rc = f(self._ref, args, stream)
         else:
             import torch
             with torch.cuda.device(self._index):
-                rc = f(self._ref, *args, self._current_stream(self._index) if stream is None else stream)
+                rc = f(self._ref, args, stream)
         if rc:
             _op(rc)
 
@@ -698,7 +708,7 @@ def paged_kv_append(cache: PagedKV, k, v, positions, seqs=None, q=None, q_out=No
     N, KV = k.shape[0], cache.n_kv_heads
     ldk, ldv = cache._ld("k", k, N, KV), cache._ld("v", v, N, KV)
     nh = ldq = ldqo = n_pos = rot = 0
-    pq = pqo = pcs = None
+    pq = pqo = pcs = 0
     if q is not None and q_out is not None:
         nh = q.shape[1] if q.dim() == 3 else 1
         ldq, ldqo = cache._ld("q", q, N, nh), cache._ld("q_out", q_out, N, nh)
@@ -708,9 +718,9 @@ def paged_kv_append(cache: PagedKV, k, v, positions, seqs=None, q=None, q_out=No
     if cos_sin is not None:
         pcs = cache._floats("cos_sin", cos_sin, cos_sin.shape if cos_sin.dim() == 2 else ("n_positions", "rot_dim"))
         n_pos, rot = cos_sin.shape
-    cache._call(cache._append, k.data_ptr(), ldk, v.data_ptr(), ldv, pq, ldq, pqo, ldqo, nh, N,
-                cache._ints("positions", positions, N), None if seqs is None else cache._ints("seqs", seqs, N), pcs,
-                n_pos, rot, int(interleaved), stream=stream)
+    cache._call(cache._append, _PAGED_ROWS.pack(
+        k.data_ptr(), v.data_ptr(), pq, pqo, ldk, ldv, ldq, ldqo, cache._ints("positions", positions, N),
+        0 if seqs is None else cache._ints("seqs", seqs, N), pcs, N, nh, n_pos, rot, interleaved), stream)
 
 
 def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None, window: int = 0, sinks: int = 0,
@@ -731,9 +741,10 @@ def paged_attention(cache: PagedKV, q, seq_lens, out, scale: float | None = None
         ws = cache.attention_workspace(nh)
     elif ws.get_device() != cache._index or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {cache.device}")
-    cache._call(cache._attention, q.data_ptr(), ldq, nh, cache._ints("seq_lens", seq_lens, B),
-                cache._scale if scale is None else scale, window, sinks, out.data_ptr(), ldo,
-                None if lse is None else cache._floats("lse", lse, (B, nh)), ws.data_ptr(), ws.nbytes, stream=stream)
+    cache._call(cache._attention, _PAGED_QUERY.pack(
+        q.data_ptr(), out.data_ptr(), 0 if lse is None else cache._floats("lse", lse, (B, nh)),
+        cache._ints("seq_lens", seq_lens, B), ws.data_ptr(), ws.nbytes, ldq, ldo, nh, window, sinks,
+        cache._scale if scale is None else scale), stream)
 
 
 def rotation_table(n_positions: int, rot_dim: int, base: float = 10000.0, device="cuda"):

@@ -1540,50 +1540,16 @@ int gpt2_op_sample_topk(const float* logits, int64_t ld, int rows, int V, int k,
   return r ? r : r2;
 }
 
-int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const void* k, int64_t ldk, const void* v, int64_t ldv,
-                            const void* q, int64_t ldq, void* q_out, int64_t ldqo, int n_q_heads, int N,
-                            const int32_t* positions, const int32_t* seqs, const float* cos_sin, int n_positions,
-                            int rot_dim, int interleaved, void* stream) {
-  OpCtx o(stream);
-  PagedAppendArgs a{};
-  a.k = k;
-  a.v = v;
-  a.q = q;
-  a.q_out = q_out;
-  a.ldk = ldk;
-  a.ldv = ldv;
-  a.ldq = ldq;
-  a.ldqo = ldqo;
-  a.nh = n_q_heads;
-  a.rows = N;
-  a.positions = positions;
-  a.seqs = seqs;
-  a.cos_sin = cos_sin;
-  a.n_positions = n_positions;
-  a.rot = rot_dim;
-  return guarded([&] { return paged_kv_append(o.c, kv, a, interleaved != 0); });
+int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const gpt2_paged_rows* rows, void* stream) {
+  return guarded([&] { return paged_kv_append(OpCtx(stream).c, kv, rows); });
 }
 
 size_t gpt2_paged_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim) {
   return paged_attention_ws_bytes(n_seqs, n_q_heads, n_kv_heads, head_dim);
 }
 
-int gpt2_op_paged_attention(const gpt2_paged_kv* kv, const void* q, int64_t ldq, int n_q_heads,
-                            const int32_t* seq_lens, float scale, int window, int sinks, void* out, int64_t ldo,
-                            float* lse, void* ws, size_t ws_bytes, void* stream) {
-  OpCtx o(stream);
-  PagedAttnArgs a{};
-  a.q = q;
-  a.out = out;
-  a.lse = lse;
-  a.ldq = ldq;
-  a.ldo = ldo;
-  a.nh = n_q_heads;
-  a.lens = seq_lens;
-  a.scale = scale;
-  a.window = window;
-  a.sinks = sinks;
-  return guarded([&] { return paged_attention(o.c, kv, a, ws, ws_bytes); });
+int gpt2_op_paged_attention(const gpt2_paged_kv* kv, const gpt2_paged_query* query, void* stream) {
+  return guarded([&] { return paged_attention(OpCtx(stream).c, kv, query); });
 }
 
 int gpt2_op_paged_status(const gpt2_paged_kv* kv, void* stream) {

@@ -1182,9 +1182,27 @@ inline bool paged_rows_ok(const void* p, int64_t ld, int64_t heads, int hd, int6
   return p && !(reinterpret_cast<uintptr_t>(p) & 15) && ld % vn == 0 && ld >= heads * hd;
 }
 
-inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedAppendArgs a, bool pairs) {
+inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, const gpt2_paged_rows* rows) {
+  PagedAppendArgs a{};
   int r = paged_view(c, kv, &a.c);
   if (r) return r;
+  if (!rows) return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: no rows");
+  a.k = rows->k;
+  a.v = rows->v;
+  a.q = rows->q;
+  a.q_out = rows->q_out;
+  a.ldk = rows->ldk;
+  a.ldv = rows->ldv;
+  a.ldq = rows->ldq;
+  a.ldqo = rows->ldqo;
+  a.nh = rows->n_q_heads;
+  a.rows = rows->n_rows;
+  a.positions = rows->positions;
+  a.seqs = rows->seqs;
+  a.cos_sin = rows->f32_cos_sin;
+  a.n_positions = rows->n_positions;
+  a.rot = rows->rot_dim;
+  const bool pairs = rows->interleaved != 0;
   if (a.rows < 0 || a.nh < 0) return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: negative size");
   if (a.rows == 0) return GPT2_OK;
   if (!a.positions || ((reinterpret_cast<uintptr_t>(a.positions) | reinterpret_cast<uintptr_t>(a.seqs)) & 3))
@@ -1317,9 +1335,23 @@ int paged_attention_hd(const LaunchCtx& c, const gpt2_paged_kv* kv, const PagedA
                       : paged_attention_inst<float, HD, 8, BOX>(c, kv, a, ws);
 }
 
-inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedAttnArgs a, void* ws, size_t ws_bytes) {
+inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, const gpt2_paged_query* query) {
+  PagedAttnArgs a{};
   int r = paged_view(c, kv, &a.c);
   if (r) return r;
+  if (!query) return fail(c, GPT2_ERR_CONFIG, "paged_attention: no query");
+  a.q = query->q;
+  a.out = query->out;
+  a.lse = query->f32_lse;
+  a.ldq = query->ldq;
+  a.ldo = query->ldo;
+  a.nh = query->n_q_heads;
+  a.lens = query->seq_lens;
+  a.scale = query->scale;
+  a.window = query->window;
+  a.sinks = query->sinks;
+  void* ws = query->ws;
+  const size_t ws_bytes = query->ws_bytes;
   if (!paged_heads_ok(a.nh, a.c.nkv))
     return fail(c, GPT2_ERR_CONFIG, "paged_attention: n_q_heads must be a multiple of n_kv_heads, at most 4096");
   if (!(a.scale > 0.f) || !(a.scale <= 1e38f) || a.window < 0 || a.sinks < 0)
