@@ -1347,15 +1347,19 @@ inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, const gp
   a.ldo = query->ldo;
   a.nh = query->n_q_heads;
   a.lens = query->seq_lens;
-  a.scale = query->scale;
+  const float scale = query->scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const double ln = (double)scale / (double)a.scale_log2;
+  a.ln_hi = (float)ln;
+  a.ln_lo = (float)(ln - (double)a.ln_hi);
   a.window = query->window;
   a.sinks = query->sinks;
   void* ws = query->ws;
   const size_t ws_bytes = query->ws_bytes;
   if (!paged_heads_ok(a.nh, a.c.nkv))
     return fail(c, GPT2_ERR_CONFIG, "paged_attention: n_q_heads must be a multiple of n_kv_heads, at most 4096");
-  if (!(a.scale > 0.f) || !(a.scale <= 1e38f) || a.window < 0 || a.sinks < 0)
-    return fail(c, GPT2_ERR_CONFIG, "paged_attention: 0 < scale <= 1e38, window >= 0, sinks >= 0");
+  if (!(scale >= 1e-30f) || !(scale <= 1e38f) || a.window < 0 || a.sinks < 0)
+    return fail(c, GPT2_ERR_CONFIG, "paged_attention: 1e-30 <= scale <= 1e38, window >= 0, sinks >= 0");
   if (kv->n_seqs == 0) return GPT2_OK;
   if (!a.lens || ((reinterpret_cast<uintptr_t>(a.lens) | reinterpret_cast<uintptr_t>(a.lse)) & 3))
     return fail(c, GPT2_ERR_CONFIG, "paged_attention: seq_lens are required; they and lse must be 4-byte aligned");

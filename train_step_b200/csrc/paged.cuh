@@ -178,9 +178,16 @@ struct PagedAttnArgs {
   int64_t ldq, ldo;
   int nh;
   const int* lens;
-  float scale;
   int window, sinks;
+  // scale * log2 e, and scale divided by it (about ln 2) as a sum of two: maxima are held in log2
+  // units, and these give them back without the error of a rounded constant
+  float scale_log2, ln_hi, ln_lo;
 };
+
+// The natural logarithm of l 2^m, m in the units of scale_log2 (l = 0: no visible key).
+__device__ __forceinline__ float pat_lse(const PagedAttnArgs& a, float m, float l) {
+  return l == 0.f ? -INFINITY : fmaf(m, a.ln_hi, fmaf(m, a.ln_lo, logf(l)));
+}
 
 // Work split. A call has one item per (sequence, key head, tile of up to QR query heads of
 // that key head's group); an item is a run of 16-key tiles over its visible keys. The tiles of
@@ -667,13 +674,14 @@ struct PatWarp<float, HD, QR> {
   }
 };
 
-// Where a worker's results for one item go: the output (whole items) or a partial result.
+// Where a worker's results for one item go: the output (whole items) or a piece.
 template <class T>
 struct PatOut {
+  const PagedAttnArgs& a;
   int rows;     // query rows of the item
-  T* out;       // row 0 of the item's output, or nullptr for a partial result
+  T* out;       // row 0 of the item's output, or nullptr for a piece
   float* lse;   // its row 0 (nullable)
-  float* part;  // row 0 of the partial result
+  float* part;  // row 0 of the piece
   float2* ml;
   int hd;
   __device__ __forceinline__ float stat(int row, float m, float l, bool first) const {
@@ -682,7 +690,7 @@ struct PatOut {
       return 1.f;
     }
     // l is 0 when every page id was bad
-    if (first && lse) lse[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    if (first && lse) lse[row] = pat_lse(a, m, l);
     return l == 0.f ? 0.f : 1.f / l;
   }
   __device__ __forceinline__ void pair(int row, int d, float x, float y) const {
@@ -724,17 +732,15 @@ struct PatSum {
       o.w = fmaf(x[i].w, g, o.w);
     }
   }
-  __device__ __forceinline__ void store(bf16* to, float* lse) const {
-    const float f = scale(lse);
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-  }
-  __device__ __forceinline__ void store(float* to, float* lse) const {
-    const float f = scale(lse);
-    *reinterpret_cast<float4*>(to) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-  }
-  __device__ __forceinline__ float scale(float* lse) const {
-    if (lse) *lse = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
-    return l == 0.f ? 0.f : 1.f / l;
+  // to `to`, and the logarithm of the sum to lse (nullable)
+  template <class T>
+  __device__ __forceinline__ void store(const PagedAttnArgs& a, T* to, float* lse) const {
+    if (lse) *lse = pat_lse(a, m, l);
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+    else
+      *reinterpret_cast<float4*>(to) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
   }
 };
 
@@ -744,7 +750,7 @@ struct PatSum {
 // `rounds` rounds; `scratch` has 24 bytes per thread.
 constexpr int PAJ_AHEAD = 8;
 template <class T, int HD>
-__device__ __forceinline__ void pat_join(const PagedAttnPlan& pl, int c0, int c1, int rows, T* out, float* lse,
+__device__ __forceinline__ void pat_join(const PagedAttnArgs& a, const PagedAttnPlan& pl, int c0, int c1, int rows, T* out, float* lse,
                                          char* scratch, int t, int threads, int rounds) {
   constexpr int VEC = HD / 4;
   float4* s_o = reinterpret_cast<float4*>(scratch);
@@ -784,7 +790,7 @@ __device__ __forceinline__ void pat_join(const PagedAttnPlan& pl, int c0, int c1
         const float4 x[1] = {s_o[threadIdx.x + i * cols]};
         sum.add(ml, x);
       }
-      sum.store(out + row * HD + v * 4, lse && v == 0 ? lse + row : nullptr);
+      sum.store(a, out + row * HD + v * 4, lse && v == 0 ? lse + row : nullptr);
     }
     __syncthreads();
   }
@@ -963,7 +969,6 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       if (word[1]) pat_claim(word[1], seen_word[1], pl.tag);
     }
     PagedCursor c = first;
-    const float scale_log2 = a.scale * 1.4426950408889634f;
     PatWarp<T, HD, QR> pw(side);
     int stage = 0, from = 0;
     uint32_t parity = 0;
@@ -1001,7 +1006,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
         pw.begin(ring + S::RING + stage * pl.rows * S::ROW, pl.rows, lane);
         from = c.tile;
       }
-      pw.tile(ks, ks + S::TILE, mask, scale_log2, lane);
+      pw.tile(ks, ks + S::TILE, mask, a.scale_log2, lane);
       __syncwarp();
       if (t + STAGES < n && !dead) {
         copy_tile(stage, pc.tile == 0);
@@ -1014,7 +1019,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
         const bool whole = end && from == 0;
         // the tail piece goes to the ring, which is done with
         char* piece = from == 0 ? ring : head;
-        PatOut<T> out;
+        PatOut<T> out{a};
         out.rows = min(QR, pl.group - q0);
         out.out = whole ? static_cast<T*>(a.out) + c.seq * a.ldo + h * HD : nullptr;
         out.lse = a.lse ? a.lse + (int64_t)c.seq * a.nh + h : nullptr;
@@ -1071,7 +1076,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       sum.add(ml, x);
     }
     if (k > 0 && sp.b1 == (int)blockIdx.x) {
-      sum.store(static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD + col * 4,
+      sum.store(a, static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD + col * 4,
                 a.lse && v == 0 ? a.lse + (int64_t)sp.seq * a.nh + sp.h + row : nullptr);
     } else {
       const int64_t slot = ((int64_t)blockIdx.x * 2 + (k > 0 ? 1 : 0)) * pl.rows;
@@ -1102,7 +1107,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
   const int threads = both ? blockDim.x / 2 : blockDim.x;
   const int i = both ? (int)threadIdx.x >= threads : !s_last[0];
   const Split sp = s_split[s_cross[i]];
-  pat_join<T, HD>(pl, sp.b0, sp.b1, sp.rows, static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD,
+  pat_join<T, HD>(a, pl, sp.b0, sp.b1, sp.rows, static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD,
                   a.lse ? a.lse + (int64_t)sp.seq * a.nh + sp.h : nullptr, pat_smem, threadIdx.x - (both ? i * threads : 0),
                   threads, (cols + threads - 1) / threads);
 }
