@@ -191,6 +191,16 @@ def test_attention_of_empty_sequences_only(dtype):
 
 
 @pytest.mark.parametrize("dtype", BOTH)
+def test_calls_on_no_sequences(dtype):
+    kc, vc = (torch.zeros(4, 16, 2, 64, dtype=dtype, device="cuda") for _ in range(2))
+    kv = tsb.PagedKV(kc, vc, torch.zeros(0, 3, dtype=torch.int32, device="cuda"))
+    q, n = torch.zeros(0, 4, 64, dtype=dtype, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
+    tsb.paged_attention(kv, q, n, torch.empty_like(q), lse=torch.empty(0, 4, device="cuda"))
+    tsb.paged_kv_append(kv, q[:, :2], q[:, 2:], n, q=q, q_out=q)
+    kv.check()
+
+
+@pytest.mark.parametrize("dtype", BOTH)
 def test_attention_of_extreme_scores(dtype):
     # one key dominates by hundreds of units; large negative scores; a scale of its own
     attention_case([300, 77], 4, 2, 64, 16, dtype, "heads", scale=1.0, q_scale=20.0, seed=3)

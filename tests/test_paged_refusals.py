@@ -108,6 +108,7 @@ def test_attention_refuses(change, code):
 
 def test_attention_of_no_sequences_does_nothing():
     assert attend(cache(n_seqs=0)) == 0
+    assert attend(cache(n_seqs=0, page_table=None), lens=None, q=None) == 0
 
 
 def test_workspace_size():
@@ -229,6 +230,20 @@ def test_index_arithmetic(tmp_path):
     subprocess.run(["g++", "-O1", "-std=c++17", "-x", "c++", "-I" + os.path.join(ROOT, "train_step_b200", "csrc"),
                     str(src), "-o", str(exe)], check=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_rotation_table_of_far_positions():
+    import numpy as np
+    n, rot = 200001, 48
+    got = tsb.rotation_table(n, rot, base=500000.0, device="cpu").numpy()
+    assert got.shape == (n, rot) and got.dtype == np.float32
+    for t in (0, 1, 4095, 131071, 200000):
+        for i in (0, 1, 11, 23):
+            angle = np.longdouble(t) * np.longdouble(500000.0) ** (-np.longdouble(2 * i) / rot)
+            # one rounding to fp32, and the angle's own in float64 (t of them at most 2^18, 53 bits)
+            for x, want in ((got[t, i], np.cos(angle)), (got[t, rot // 2 + i], np.sin(angle))):
+                assert abs(float(x) - float(want)) <= 2.0 ** -24 * abs(float(want)) + 2.0 ** -33
+    assert tsb.rotation_table(5, 0, device="cpu").shape == (5, 0)
 
 
 def test_binding_refuses_what_is_not_on_a_gpu():

@@ -1146,7 +1146,7 @@ inline bool paged_head_dim_ok(int hd) { return hd == 32 || hd == 64 || hd == 96 
 
 // Checks a caller's cache description and fills the kernels' view of it.
 inline int paged_view(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedView* out) {
-  if (!kv || !kv->k || !kv->v || !kv->page_table)
+  if (!kv || !kv->k || !kv->v || (!kv->page_table && kv->n_seqs != 0))
     return fail(c, GPT2_ERR_CONFIG, "paged cache: k, v and page_table are required");
   if (kv->dtype != GPT2_BF16 && kv->dtype != GPT2_FP32)
     return fail(c, GPT2_ERR_CONFIG, "paged cache: dtype must be GPT2_FP32 or GPT2_BF16");

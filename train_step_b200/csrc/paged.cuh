@@ -398,8 +398,10 @@ __device__ __forceinline__ int64_t pat_item_start(const int* before, int n_seqs,
 template <class T, int HD, int QR>
 struct PatWarp;
 
-// bf16: m16n8k16 tensor-core products. S = Q K^T: the query heads are the 16-row operand, a
-// tile's keys two 8-column operands. P V: the weights a lane holds after S are exactly the
+// bf16: m16n8k16 tensor-core products (a key head has at most 16 query rows: the 128-row products
+// of the accumulator-memory kind would be at least 7/8 empty, and S and P would travel through
+// that memory). S = Q K^T: the query heads are the 16-row operand, a tile's keys two 8-column
+// operands. P V: the weights a lane holds after S are exactly the
 // first operand's fragment. The weights are not rounded to one bf16: with up to 8 query heads
 // (QR 8) rows 8..15 of the operand, otherwise empty, hold the remainders p - bf16(p), and the
 // two halves of the result are added at the end; with up to 16 heads the remainders take a
