@@ -181,6 +181,19 @@ def test_attention_through_large_windows(dtype, window, sinks):
     attention_case([5000, 1100, 77, 3001], 4, 2, 64, 16, dtype, "heads", window, sinks, seed=window)
 
 
+@pytest.mark.parametrize("layout", ["heads", "tokens", "padded"])
+@pytest.mark.parametrize("NH,nkv,page", [(2, 2, 16), (3, 3, 32), (5, 5, 16), (12, 3, 64), (56, 7, 16), (6, 3, 8)])
+def test_attention_of_pairs_of_small_heads(NH, nkv, page, layout):
+    # an odd head alone in its pair: split over warps and blocks, in windows, beside padding rows
+    # that nothing may write
+    for lens, window, sinks in (([1, 37, 0, 150, 16], 0, 0), ([2500, 1, 40, 0, 1800], 0, 0), ([900, 5, 0, 333], 200, 9)):
+        kv, q, ln, out, lse, ref = attention_case(lens, NH, nkv, 32, page, torch.bfloat16, layout, window, sinks,
+                                                  seed=NH + page)
+        wide = torch.full((len(lens), NH + 16, 32), 7.0, dtype=torch.bfloat16, device="cuda")
+        tsb.paged_attention(kv, q, ln, wide[:, :NH], window=window, sinks=sinks)
+        assert torch.equal(wide[:, :NH], out) and (wide[:, NH:] == 7).all()
+
+
 def test_attention_more_sequences_than_workers():
     attention_case([(i * 13) % 40 for i in range(700)], 5, 5, 32, 8, torch.bfloat16, "heads", seed=8)
 

@@ -1241,11 +1241,21 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, const gp
 
 inline bool paged_heads_ok(int nh, int nkv) { return nkv >= 1 && nh >= 1 && nh <= 4096 && nh % nkv == 0; }
 
-// Partial results of at most PAT_MAX_BLOCKS blocks: two each, of min(16, group) rows; and an
+// Key heads of an item (of bf16 caches read by tensor copies): two of 32 elements, else one. A
+// tile of one such head is 1 KB of keys, and what a tile costs besides its bytes bounds the call:
+// 64 sequences of 512 to 8192 tokens, 16 key heads, 366 MB: 103 us with one, 68 with two, 72 to 76
+// with four; a single short sequence 5.2 and 5.7 us with one and two. With heads of 64 elements
+// pairs cost more in registers than they save (90 -> 96 us).
+constexpr int paged_heads_of(int hd) { return hd == 32 ? 2 : 1; }
+inline int paged_heads_per_item(int nkv, int group, int hd) {
+  return group <= 8 && nkv >= paged_heads_of(hd) ? paged_heads_of(hd) : 1;
+}
+
+// Partial results of at most PAT_MAX_BLOCKS blocks: two each, of an item's query rows; and an
 // arrival word each.
 inline size_t paged_attention_ws_bytes(int n_seqs, int nh, int nkv, int hd) {
   if (n_seqs < 0 || n_seqs > PAGED_MAX_SEQS || !paged_heads_ok(nh, nkv) || !paged_head_dim_ok(hd)) return 0;
-  const size_t rows = std::min(16, nh / nkv);
+  const size_t rows = paged_heads_per_item(nkv, nh / nkv, hd) * std::min(16, nh / nkv);
   return (size_t)PAT_MAX_BLOCKS * (8 + 2 * rows * (8 + (size_t)hd * 4));
 }
 
@@ -1262,10 +1272,11 @@ inline unsigned long long paged_call_tag() {
   return z & ~PAT_COUNT;
 }
 
-// A pool as a 4-D tensor {head_dim, page_size, n_kv_heads, n_pages}; box: 16 tokens of one head
-// and page, up to 128 bytes wide. A stride of a dimension of one element is not used; false for
-// strides that a tensor map does not take (0, as of an expanded tensor, or 2^40 bytes and more).
-inline bool encode_paged_map(CUtensorMap* map, const void* ptr, const gpt2_paged_kv* kv) {
+// A pool as a 4-D tensor {head_dim, page_size, n_kv_heads, n_pages}; box: 16 tokens of `heads`
+// heads (those past the last read as zero) of a page, up to 128 bytes wide. A stride of a dimension
+// of one element is not used; false for strides that a tensor map does not take (0, as of an
+// expanded tensor, or 2^40 bytes and more).
+inline bool encode_paged_map(CUtensorMap* map, const void* ptr, const gpt2_paged_kv* kv, int heads) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const bool bf = kv->dtype == GPT2_BF16;
@@ -1278,7 +1289,7 @@ inline bool encode_paged_map(CUtensorMap* map, const void* ptr, const gpt2_paged
   for (cuuint64_t s : strides)
     if (s == 0) return false;
   const int row = (int)std::min<int64_t>(128, kv->head_dim * es);
-  cuuint32_t box[4] = {(cuuint32_t)(row / es), (cuuint32_t)PAT_TILE, 1u, 1u};
+  cuuint32_t box[4] = {(cuuint32_t)(row / es), (cuuint32_t)PAT_TILE, (cuuint32_t)heads, 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   return enc(map, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(ptr),
              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1286,23 +1297,23 @@ inline bool encode_paged_map(CUtensorMap* map, const void* ptr, const gpt2_paged
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, int HD, int QR, bool BOX>
+template <class T, int HD, int QR, int HP, bool BOX>
 int paged_attention_inst(const LaunchCtx& c, const gpt2_paged_kv* kv, const PagedAttnArgs& a, void* ws) {
-  using S = PatShape<T, HD, QR>;
-  static_assert(S::warps(QR, PAGED_MAX_SEQS) >= 1, "rings too large");
+  using S = PatShape<T, HD, QR, HP>;
+  static_assert(S::warps(HP * QR, PAGED_MAX_SEQS) >= 1, "rings too large");
   CUtensorMap km{}, vm{};
-  if (BOX && (!encode_paged_map(&km, kv->k, kv) || !encode_paged_map(&vm, kv->v, kv)))
-    return paged_attention_inst<T, HD, QR, false>(c, kv, a, ws);
-  if (!smem_optin(paged_attn_kernel<T, HD, QR, BOX>, PAT_SMEM))
+  if (BOX && (!encode_paged_map(&km, kv->k, kv, HP) || !encode_paged_map(&vm, kv->v, kv, HP)))
+    return paged_attention_inst<T, HD, QR, 1, false>(c, kv, a, ws);
+  if (!smem_optin(paged_attn_kernel<T, HD, QR, HP, BOX>, PAT_SMEM))
     return fail(c, GPT2_ERR_CUDA, "paged_attention: shared memory opt-in failed");
   PagedAttnPlan pl;
   pl.group = a.nh / a.c.nkv;
-  pl.rows = std::min(QR, pl.group);
+  pl.rows = HP * std::min(QR, pl.group);
   pl.warps = S::warps(pl.rows, a.c.n_seqs);
   const int grid = std::min(c.num_sms, PAT_MAX_BLOCKS);
   pl.workers = grid * pl.warps;
   pl.qtiles = (pl.group + QR - 1) / QR;
-  pl.items = a.c.nkv * pl.qtiles;
+  pl.items = (a.c.nkv + HP - 1) / HP * pl.qtiles;
   pl.per_item = 0xffffffffu / pl.items;
   pl.per_worker = 0xffffffffu / pl.workers;
   pl.per_block = 0xffffffffu / grid;
@@ -1315,7 +1326,7 @@ int paged_attention_inst(const LaunchCtx& c, const gpt2_paged_kv* kv, const Page
   pl.arrived = reinterpret_cast<unsigned long long*>(p);
   LaunchCtx cp = c;
   cp.pdl = true;
-  const cudaError_t e = launch_k(cp, paged_attn_kernel<T, HD, QR, BOX>, dim3(grid), dim3(pl.warps * 32),
+  const cudaError_t e = launch_k(cp, paged_attn_kernel<T, HD, QR, HP, BOX>, dim3(grid), dim3(pl.warps * 32),
                                  S::smem(pl.rows, a.c.n_seqs), a, pl, km, vm);
   if (e != cudaSuccess) return fail(c, GPT2_ERR_CUDA, std::string("paged_attention: ") + cudaGetErrorString(e));
   return check_launch(c, "paged_attention");
@@ -1327,12 +1338,16 @@ int paged_attention_inst(const LaunchCtx& c, const gpt2_paged_kv* kv, const Page
 template <int HD, bool BOX>
 int paged_attention_hd(const LaunchCtx& c, const gpt2_paged_kv* kv, const PagedAttnArgs& a, void* ws) {
   const int group = a.nh / a.c.nkv;
-  if (kv->dtype == GPT2_BF16)
-    return group <= 8 ? paged_attention_inst<bf16, HD, 8, BOX>(c, kv, a, ws)
-                      : paged_attention_inst<bf16, HD, 16, BOX>(c, kv, a, ws);
-  return group == 1   ? paged_attention_inst<float, HD, 1, BOX>(c, kv, a, ws)
-         : group <= 4 ? paged_attention_inst<float, HD, 4, BOX>(c, kv, a, ws)
-                      : paged_attention_inst<float, HD, 8, BOX>(c, kv, a, ws);
+  if (kv->dtype == GPT2_BF16) {
+    constexpr int HP = BOX ? paged_heads_of(HD) : 1;
+    if (HP > 1 && paged_heads_per_item(a.c.nkv, group, HD) == HP)
+      return paged_attention_inst<bf16, HD, 8, HP, BOX>(c, kv, a, ws);
+    return group <= 8 ? paged_attention_inst<bf16, HD, 8, 1, BOX>(c, kv, a, ws)
+                      : paged_attention_inst<bf16, HD, 16, 1, BOX>(c, kv, a, ws);
+  }
+  return group == 1   ? paged_attention_inst<float, HD, 1, 1, BOX>(c, kv, a, ws)
+         : group <= 4 ? paged_attention_inst<float, HD, 4, 1, BOX>(c, kv, a, ws)
+                      : paged_attention_inst<float, HD, 8, 1, BOX>(c, kv, a, ws);
 }
 
 inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, const gpt2_paged_query* query) {

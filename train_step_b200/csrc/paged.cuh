@@ -190,7 +190,8 @@ __device__ __forceinline__ float pat_lse(const PagedAttnArgs& a, float m, float 
 }
 
 // Work split. A call has one item per (sequence, key head, tile of up to QR query heads of
-// that key head's group); an item is a run of 16-key tiles over its visible keys. The tiles of
+// that key head's group), or per (sequence, HP key heads with their groups) where heads are
+// small; an item is a run of 16-key tiles over its visible keys. The tiles of
 // all items are laid end to end and every warp of the grid (a worker) takes an equal,
 // contiguous share of them, so ragged lengths balance without the host knowing them. A worker
 // that takes an item whole writes its output. Otherwise it leaves pieces in shared memory: at
@@ -218,16 +219,19 @@ __device__ __forceinline__ float pat_lse(const PagedAttnArgs& a, float m, float 
 constexpr int PAT_MAX_BLOCKS = 256;
 constexpr int PAT_SMEM = 226 * 1024;  // of a block
 
-template <class T, int HD, int QR_>
+template <class T, int HD, int QR_, int HP_ = 1>
 struct PatShape {
-  static constexpr int QR = QR_;              // query rows of an item, at most
+  static constexpr int QR = QR_;              // query rows of a key head, at most
+  static constexpr int HP = HP_;              // key heads of an item
   static constexpr int ROW = HD * sizeof(T);  // bytes
   static constexpr int CPR = ROW / 16;        // 16-byte chunks per row
-  // keys (and values) of a tile: boxes of 16 rows of up to 128 bytes
+  // keys (and values) of a tile: for each key head, boxes of 16 rows of up to 128 bytes
   static constexpr int BOX_ROW = ROW < 128 ? ROW : 128;
   static constexpr int BOXES = (ROW + BOX_ROW - 1) / BOX_ROW;
   static constexpr int BOX = PAT_TILE * BOX_ROW;
-  static constexpr int TILE = BOXES * BOX;
+  static constexpr int SUB = BOXES * BOX;  // one key head
+  static constexpr int TILE = HP * SUB;
+  static_assert(HP == 1 || BOXES == 1, "several heads in one copy");
   static constexpr int STAGES = 2;  // 3: 224 -> 244 us on the 1.46 GB above, with as many warps
   // fp32: a copy of the item's queries and the tile's weights, per warp
   static constexpr int SIDE = sizeof(T) == 4 ? QR * ROW + QR * PAT_TILE * 4 : 0;
@@ -252,8 +256,8 @@ struct PatShape {
   static constexpr int smem(int rows, int n_seqs) {
     return 1024 + warps(rows, n_seqs) * warp_bytes(rows) + (n_seqs + 1) * 4;
   }
-  // the smallest group that comes to this shape
-  static constexpr int MIN_ROWS = sizeof(T) == 2 ? (QR == 16 ? 9 : 1) : QR == 8 ? 5 : QR == 4 ? 2 : 1;
+  // the fewest rows that come to this shape
+  static constexpr int MIN_ROWS = HP > 1 ? HP : sizeof(T) == 2 ? (QR == 16 ? 9 : 1) : QR == 8 ? 5 : QR == 4 ? 2 : 1;
   static constexpr int MAX_WARPS = warps(MIN_ROWS, 1);
 
   // 16-byte chunk `c` of row `r` in a tile: the order in which a tensor copy with 128-byte (64-byte
@@ -266,7 +270,7 @@ struct PatShape {
 
 struct PagedAttnPlan {
   int warps;    // of a block
-  int workers, items, qtiles, group, rows;  // rows: min(QR, group), the rows of a partial result
+  int workers, items, qtiles, group, rows;  // rows: HP min(QR, group), the rows of a partial result
   uint32_t per_item, per_worker, per_block; // inverses of items, workers and blocks, for paged_div_by
   unsigned long long tag;                   // of this call, above the bits of PAT_COUNT
   unsigned long long* arrived;              // [blocks]: see pat_claim
@@ -418,7 +422,7 @@ struct PatWarp<bf16, HD, QR> {
   float acc[NT][4];
   float m[RV], l[RV];
 
-  __device__ __forceinline__ PatWarp(char*) {}
+  __device__ __forceinline__ void init(char*) {}
   __device__ __forceinline__ void begin(const char* q, int rows, int lane) {
     const uint32_t qs = smem_u32(q);
     // rows 0..7 (and 8..15) of Q as first-operand fragments; rows that do not exist repeat row 0
@@ -578,7 +582,7 @@ struct PatWarp<float, HD, QR> {
   float4* qb;  // [QR][CPR]
   float* wb;   // [QR][PAT_TILE]
 
-  __device__ __forceinline__ PatWarp(char* side) {
+  __device__ __forceinline__ void init(char* side) {
     qb = reinterpret_cast<float4*>(side);
     wb = reinterpret_cast<float*>(side + QR * HD * 4);
   }
@@ -798,11 +802,12 @@ __device__ __forceinline__ void pat_join(const PagedAttnArgs& a, const PagedAttn
   }
 }
 
-template <class T, int HD, int QR, bool BOX>
-__global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
+template <class T, int HD, int QR, int HP, bool BOX>
+__global__ void __launch_bounds__(PatShape<T, HD, QR, HP>::MAX_WARPS * 32, 1)
     paged_attn_kernel(const PagedAttnArgs a, const PagedAttnPlan pl, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
-  using S = PatShape<T, HD, QR>;
+  using S = PatShape<T, HD, QR, HP>;
+  static_assert(HP == 1 || BOX, "several heads come by tensor copies");
   constexpr int CPR = S::CPR, STAGES = S::STAGES, VN = 16 / sizeof(T);
   constexpr uint64_t LIMIT_NS = 2000000000ull;  // a wait gives up after two seconds
   extern __shared__ char pat_raw[];
@@ -902,10 +907,17 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
         // (the bound: a length that changes during the call must not lead out of the table)
         page = a.c.table[pc.seq * a.c.table_stride + min(mine >> a.c.log2_page, a.c.max_pages - 1)];
     };
+    // the item's first key head, the first row of its tile of the group, its query rows
+    auto heads = [&](const PagedCursor& at, int& hk, int& q0, int& rows) {
+      const int k = pl.qtiles == 1 ? at.item : at.item / pl.qtiles;
+      hk = k * HP;
+      q0 = (at.item - k * pl.qtiles) * QR;
+      rows = HP == 1 ? min(QR, pl.group - q0) : min(HP, a.c.nkv - hk) * pl.group;
+    };
     auto copy_tile = [&](int stage, bool with_q) {
       const uint32_t seen = paged_tile_mask(vis, pos);
-      const int hk = pl.qtiles == 1 ? pc.item : pc.item / pl.qtiles;
-      const int q0 = (pc.item - hk * pl.qtiles) * QR, rows = min(QR, pl.group - q0);  // of the group
+      int hk, q0, rows;
+      heads(pc, hk, q0, rows);
       const T* q = static_cast<const T*>(a.q) + pc.seq * a.ldq + (hk * pl.group + q0) * HD;
       char* qs = ring + S::RING + stage * pl.rows * S::ROW;
       char* ks = ring + stage * 2 * S::TILE;
@@ -971,7 +983,9 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       if (word[1]) pat_claim(word[1], seen_word[1], pl.tag);
     }
     PagedCursor c = first;
-    PatWarp<T, HD, QR> pw(side);
+    PatWarp<T, HD, QR> pw[HP];
+#pragma unroll
+    for (int i = 0; i < HP; ++i) pw[i].init(side);
     int stage = 0, from = 0;
     uint32_t parity = 0;
     bool dead = false;
@@ -998,17 +1012,23 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       if (BOX && mask != 0xffffu) {
         // what a page holds in place of unseen keys may be anything: their weights are 0, and
         // their values must not be infinite or NaN
-        for (int i = lane; i < PAT_TILE * CPR; i += 32)
-          if (!(mask >> (i / CPR) & 1))
-            *reinterpret_cast<uint4*>(ks + S::TILE + S::chunk(i / CPR, i % CPR)) = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = lane; i < HP * PAT_TILE * CPR; i += 32) {
+          const int row = i / CPR % PAT_TILE;
+          if (!(mask >> row & 1))
+            *reinterpret_cast<uint4*>(ks + S::TILE + i / (PAT_TILE * CPR) * S::SUB + S::chunk(row, i % CPR)) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
         fence_proxy_async_smem();  // before the next copy into this stage
         __syncwarp();
       }
       if (t == 0 || c.tile == 0) {
-        pw.begin(ring + S::RING + stage * pl.rows * S::ROW, pl.rows, lane);
+#pragma unroll
+        for (int i = 0; i < HP; ++i)
+          pw[i].begin(ring + S::RING + (stage * pl.rows + i * pl.group) * S::ROW, HP == 1 ? pl.rows : pl.group, lane);
         from = c.tile;
       }
-      pw.tile(ks, ks + S::TILE, mask, a.scale_log2, lane);
+#pragma unroll
+      for (int i = 0; i < HP; ++i) pw[i].tile(ks + i * S::SUB, ks + S::TILE + i * S::SUB, mask, a.scale_log2, lane);
       __syncwarp();
       if (t + STAGES < n && !dead) {
         copy_tile(stage, pc.tile == 0);
@@ -1017,22 +1037,28 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR>::MAX_WARPS * 32, 1)
       if (!BOX) cp_async_commit();
       const bool end = c.tile == c.tiles - 1;
       if (end || t == n - 1) {
-        const int hk = c.item / pl.qtiles, q0 = (c.item - hk * pl.qtiles) * QR, h = hk * pl.group + q0;
+        int hk, q0, rows;
+        heads(c, hk, q0, rows);
+        const int h = hk * pl.group + q0;
         const bool whole = end && from == 0;
         // the tail piece goes to the ring, which is done with
         char* piece = from == 0 ? ring : head;
-        PatOut<T> out{a};
-        out.rows = min(QR, pl.group - q0);
-        out.out = whole ? static_cast<T*>(a.out) + c.seq * a.ldo + h * HD : nullptr;
-        out.lse = a.lse ? a.lse + (int64_t)c.seq * a.nh + h : nullptr;
-        out.part = reinterpret_cast<float*>(piece);
-        out.ml = reinterpret_cast<float2*>(piece + pl.rows * HD * 4);
-        out.hd = HD;
-        pw.finish(lane, out);
+#pragma unroll
+        for (int i = 0; i < HP; ++i) {
+          const int r0 = i * pl.group;  // its first row
+          PatOut<T> out{a};
+          out.rows = HP == 1 ? rows : min(pl.group, rows - r0);
+          out.out = whole ? static_cast<T*>(a.out) + c.seq * a.ldo + (h + r0) * HD : nullptr;
+          out.lse = a.lse ? a.lse + (int64_t)c.seq * a.nh + h + r0 : nullptr;
+          out.part = reinterpret_cast<float*>(piece) + r0 * HD;
+          out.ml = reinterpret_cast<float2*>(piece + pl.rows * HD * 4) + r0;
+          out.hd = HD;
+          pw[i].finish(lane, out);
+        }
         if (!whole && lane == 0 && (from == 0 || warp == 0)) {
           const int64_t start = u0 + t - c.tile, last = start + c.tiles - 1;  // the item's first and last tile
           const int k = from == 0 ? warp + 1 : 0;
-          Split sp{c.seq, h, out.rows, (int)blockIdx.x, (int)blockIdx.x, from == 0 ? warp : 0, pl.warps - 1};
+          Split sp{c.seq, h, rows, (int)blockIdx.x, (int)blockIdx.x, from == 0 ? warp : 0, pl.warps - 1};
           if (last < a1) sp.p1 = (int)paged_div(last - a0, share);
           if (k == 0) sp.b0 = (int)paged_div(start, range);
           if (last >= a1) sp.b1 = (int)paged_div(last, range);
