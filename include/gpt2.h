@@ -466,7 +466,9 @@ typedef struct {
  * same row stride, but not overlap it otherwise). A row whose position, sequence, table entry or
  * rotation row is outside its range is skipped and raises the status word; rows that are skipped
  * leave q_out as it was. Rows must name distinct slots: of two rows for one slot, each 16 bytes
- * come from either. Row bases and strides (elements) are multiples of 16 bytes; n_rows *
+ * come from either. The cache's strides must keep its heads apart, each stepping over what the
+ * smaller ones span (GPT2_ERR_CONFIG: an expanded tensor can be read, not appended to), and k
+ * and v may not share elements. Row bases and strides (elements) are multiples of 16 bytes; n_rows *
  * (n_q_heads + 2 n_kv_heads) * head_dim elements are at most 32 GB (GPT2_ERR_BATCH). The struct
  * is read during the call only. */
 typedef struct {

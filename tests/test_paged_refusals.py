@@ -89,6 +89,23 @@ def test_append_refuses(change, code):
     assert b"paged_kv_append" in tsb.lib().gpt2_op_last_error()
 
 
+@pytest.mark.parametrize("strides", [
+    dict(head_stride=0), dict(head_stride=56), dict(row_stride=64), dict(page_stride=0), dict(page_stride=1984),
+    dict(row_stride=0), dict(head_stride=2048, row_stride=64, page_stride=2048), dict(page_stride=(1 << 63) - 8)])
+def test_append_refuses_a_cache_whose_heads_overlap(strides):
+    kv = cache(**strides)
+    assert append(kv) == CONFIG and b"overlap" in tsb.lib().gpt2_op_last_error()
+    assert append(kv, N=0) == CONFIG
+
+
+@pytest.mark.parametrize("strides", [
+    dict(head_stride=0, n_kv_heads=1), dict(row_stride=0, page_size=1, max_pages=8), dict(page_stride=0, n_pages=1),
+    dict(head_stride=1024, row_stride=64), dict(page_stride=64, head_stride=6400, row_stride=12800),
+    dict(page_stride=4096)])
+def test_append_takes_any_order_of_the_cache_and_dimensions_of_one(strides):
+    assert append(cache(**strides), N=0) == 0
+
+
 def test_append_of_no_rows_does_nothing():
     assert append(cache(), N=0) == 0
     assert append(cache(), N=0, positions=None) == 0

@@ -1182,11 +1182,29 @@ inline bool paged_rows_ok(const void* p, int64_t ld, int64_t heads, int hd, int6
   return p && !(reinterpret_cast<uintptr_t>(p) & 15) && ld % vn == 0 && ld >= heads * hd;
 }
 
+// Whether no two heads of the cache share elements: each stride, from the smallest on, steps over
+// all that the smaller ones span (dimensions of one element aside). An expanded tensor's do not.
+inline bool paged_slots_apart(const gpt2_paged_kv* kv) {
+  std::pair<int64_t, int64_t> dim[3] = {
+      {kv->head_stride, kv->n_kv_heads}, {kv->row_stride, kv->page_size}, {kv->page_stride, kv->n_pages}};
+  std::sort(dim, dim + 3);
+  int64_t span = kv->head_dim;
+  for (const auto& [stride, n] : dim) {
+    if (n == 1) continue;
+    if (stride < span) return false;
+    if (stride > (INT64_MAX - span) / (n - 1)) return false;
+    span += stride * (n - 1);
+  }
+  return true;
+}
+
 inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, const gpt2_paged_rows* rows) {
   PagedAppendArgs a{};
   int r = paged_view(c, kv, &a.c);
   if (r) return r;
   if (!rows) return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: no rows");
+  if (!paged_slots_apart(kv))
+    return fail(c, GPT2_ERR_CONFIG, "paged_kv_append: the paged cache's strides let heads overlap");
   a.k = rows->k;
   a.v = rows->v;
   a.q = rows->q;
