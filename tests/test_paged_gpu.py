@@ -296,6 +296,41 @@ def test_attention_passes_on_nan(dtype, n):
     assert torch.equal(torch.isnan(got), bad) and torch.isnan(l2[0, 2:]).all() and not torch.isnan(l2[0, :2]).any()
 
 
+INFINITE = [(12, 12, 64, 16), (8, 2, 64, 16), (16, 2, 64, 16), (9, 1, 128, 16), (40, 2, 96, 64), (6, 3, 32, 16), (4, 2, 64, 8)]
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("n", [10, 5000])  # within one worker, and spread over many
+@pytest.mark.parametrize("NH,nkv,hd,page", INFINITE)
+def test_attention_of_infinite_values_in_view(dtype, n, NH, nkv, hd, page):
+    # softmax weights are positive: an infinite value is the output of its element, two of both
+    # signs have no sum, and everything else is as without them
+    kv, q, ln, out, lse, _ = attention_case([n, 33], NH, nkv, hd, page, dtype, "heads", seed=61, poison=False)
+    table = kv.page_table.cpu()
+    z = [torch.stack([kv.k_cache[int(table[0, t // page]), t % page, h] for t in range(min(n, 48))]).double().cpu()
+         @ q[0, h * (NH // nkv)].double().cpu() for h in range(nkv)]
+
+    def value(t, h):
+        return kv.v_cache[int(table[0, t // page]), t % page, h]
+
+    want = out.clone()
+    for h in range(nkv):
+        heads = slice(h * (NH // nkv), (h + 1) * (NH // nkv))
+        # of the tokens at the front, the one that scores highest (its weight can be exactly a
+        # power of two) and the lowest; and the last of all
+        for t, e, x in ((int(z[h].argmax()), 3, math.inf), (int(z[h].argmin()), 4, -math.inf), (n - 1, 11, math.inf),
+                        (0, 17, math.inf), (1, 17, math.inf), (2, 30, math.inf), (n - 1, 30, -math.inf)):
+            value(t, h)[e] = x
+            want[0, heads, e] = math.nan if e == 30 and x < 0 else x
+    got, l2 = torch.zeros_like(out), torch.zeros_like(lse)
+    tsb.paged_attention(kv, q, ln, got, lse=l2)
+    kv.check()
+    assert torch.equal(l2, lse)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    keep = ~torch.isnan(want)
+    assert torch.equal(got[keep], want[keep])
+
+
 @pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("page", [8, 16, 64])
 def test_attention_over_an_expanded_cache(dtype, page):

@@ -409,8 +409,10 @@ struct PatWarp;
 // first operand's fragment. The weights are not rounded to one bf16: with up to 8 query heads
 // (QR 8) rows 8..15 of the operand, otherwise empty, hold the remainders p - bf16(p), and the
 // two halves of the result are added at the end; with up to 16 heads the remainders take a
-// second product. P is so carried to 2^-16 of its value at no or little cost (the products
-// are far from the tensor cores' rate: the kernel is bound by reading the cache).
+// second product and sums of their own. P is so carried to 2^-16 of its value at no or little
+// cost (the products are far from the tensor cores' rate: the kernel is bound by reading the
+// cache). A remainder may be 0 or negative, and its product with an infinite value NaN or of the
+// other sign; where the first half is infinite or NaN, it is the result.
 // The running maximum moves only when a tile exceeds it by more than 8 (weights and sums against
 // an older maximum are at most 2^8 larger, and as exact), so most tiles do not rescale the output.
 template <int HD, int QR>
@@ -419,7 +421,8 @@ struct PatWarp<bf16, HD, QR> {
   static constexpr int KS = HD / 16, NT = HD / 8;
   static constexpr int RV = QR / 8;  // query rows a lane holds statistics of
   uint32_t qf[KS][2 * RV];
-  float acc[NT][4];
+  float acc[NT][4];  // QR 8: [2], [3] for the remainders
+  float rest[NT][4];  // QR 16: the remainders'
   float m[RV], l[RV];
 
   __device__ __forceinline__ void init(char*) {}
@@ -447,7 +450,10 @@ struct PatWarp<bf16, HD, QR> {
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        acc[j][i] = 0.f;
+        if (RV == 2) rest[j][i] = 0.f;
+      }
 #pragma unroll
     for (int i = 0; i < RV; ++i) {
       m[i] = -INFINITY;
@@ -509,6 +515,9 @@ struct PatWarp<bf16, HD, QR> {
           if (RV == 1) {
             acc[j][2] *= f;
             acc[j][3] *= f;
+          } else {
+            rest[j][2 * r] *= f;
+            rest[j][2 * r + 1] *= f;
           }
         }
       }
@@ -537,7 +546,7 @@ struct PatWarp<bf16, HD, QR> {
           dec_mma(acc[j + e], hi[0][0], lo[0][0], hi[0][1], lo[0][1], b[2 * e], b[2 * e + 1]);
         } else {
           dec_mma(acc[j + e], hi[0][0], hi[RV - 1][0], hi[0][1], hi[RV - 1][1], b[2 * e], b[2 * e + 1]);
-          dec_mma(acc[j + e], lo[0][0], lo[RV - 1][0], lo[0][1], lo[RV - 1][1], b[2 * e], b[2 * e + 1]);
+          dec_mma(rest[j + e], lo[0][0], lo[RV - 1][0], lo[0][1], lo[RV - 1][1], b[2 * e], b[2 * e + 1]);
         }
       }
     }
@@ -558,10 +567,9 @@ struct PatWarp<bf16, HD, QR> {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         float x = acc[j][2 * r], y = acc[j][2 * r + 1];
-        if (RV == 1) {
-          x += acc[j][2];
-          y += acc[j][3];
-        }
+        const float xr = RV == 1 ? acc[j][2] : rest[j][2 * r], yr = RV == 1 ? acc[j][3] : rest[j][2 * r + 1];
+        if (isfinite(x)) x += xr;
+        if (isfinite(y)) y += yr;
         out.pair(row, j * 8 + (lane & 3) * 2, x * f, y * f);
       }
     }
