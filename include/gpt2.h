@@ -493,7 +493,9 @@ int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const gpt2_paged_rows* rows
  * Softmax statistics and sums are fp32, each output is rounded once; a NaN in q, or in a
  * visible key or value, gives NaN where the formula does, one in an unseen place has no effect.
  * An infinite visible value gives its element that infinity (NaN beside one of the other sign;
- * a weight below 2^-80 of the largest may count as 0, and 0 times infinity is NaN).
+ * a weight below 2^-80 of the largest may count as 0, and 0 times infinity is NaN). Finite
+ * values give a finite output as long as it and its rounding error are in fp32's range; the
+ * scores (scale log2 e q.k) are fp32 too.
  * 1e-30 <= scale <= 1e38. out may not overlap q, the cache or ws. ws: DEVICE workspace of
  * gpt2_paged_attention_ws_bytes bytes, 16-byte aligned, of any content; calls that may run at
  * the same time need one each. Deterministic for given lengths. The struct is read during the

@@ -332,6 +332,35 @@ def test_attention_of_infinite_values_in_view(dtype, n, NH, nkv, hd, page):
 
 
 @pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("lens", [[10, 1, 33], [5000, 77], [20000, 1]])
+@pytest.mark.parametrize("NH,nkv,hd,page", [(12, 12, 64, 16), (16, 2, 64, 16), (6, 3, 32, 16), (8, 2, 128, 32), (4, 2, 96, 8)])
+def test_attention_of_values_near_the_largest(dtype, lens, NH, nkv, hd, page):
+    # the output is between the smallest and the largest visible value, so it is finite where the
+    # values are: bf16 at the type's largest (its rounding errors leave fp32 256 steps of room),
+    # fp32 at half of it
+    top = torch.finfo(dtype).max / (1 if dtype == torch.bfloat16 else 2)
+    kv, q, ln, out, lse, _ = attention_case(lens, NH, nkv, hd, page, dtype, "heads", seed=71, poison=False)
+    kv.v_cache.clamp_(-1, 1).mul_(top)
+    kv.v_cache[..., 0] = top
+    kv.v_cache[..., 1] = -top
+    args = (kv.v_cache.double().cpu(), kv.page_table.cpu().numpy(), q.double().cpu(), lens)
+    ref = reference(kv.k_cache.double().cpu(), *args, hd ** -0.5)
+    tsb.paged_attention(kv, q, ln, out, lse=lse)
+    check(out, lse, ref, dtype)
+    # scores that rise by 4 with every token and so leave every older maximum behind
+    for b, n in enumerate(lens):
+        for t in range(min(n, 200)):
+            kv.k_cache[int(kv.page_table[b, t // page]), t % page] = 0
+            kv.k_cache[int(kv.page_table[b, t // page]), t % page, :, 0] = 4.0 * t
+    q.zero_()
+    q[..., 0] = 1
+    args = (kv.v_cache.double().cpu(), kv.page_table.cpu().numpy(), q.double().cpu(), lens)
+    ref = reference(kv.k_cache.double().cpu(), *args, 1.0)
+    tsb.paged_attention(kv, q, ln, out, scale=1.0, lse=lse)
+    check(out, lse, ref, dtype)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("page", [8, 16, 64])
 def test_attention_over_an_expanded_cache(dtype, page):
     # one stored head shown as four (head stride 0)

@@ -180,13 +180,25 @@ struct PagedAttnArgs {
   const int* lens;
   int window, sinks;
   // scale * log2 e, and scale divided by it (about ln 2) as a sum of two: maxima are held in log2
-  // units, and these give them back without the error of a rounded constant
-  float scale_log2, ln_hi, ln_lo;
+  // units, and these give them back without the error of a rounded constant; log 2 less their sum too
+  float scale_log2, ln_hi, ln_lo, ln_off;
 };
 
-// The natural logarithm of l 2^m, m in the units of scale_log2 (l = 0: no visible key).
-__device__ __forceinline__ float pat_lse(const PagedAttnArgs& a, float m, float l) {
-  return l == 0.f ? -INFINITY : fmaf(m, a.ln_hi, fmaf(m, a.ln_lo, logf(l)));
+// How far the reference of an item's weights lies above the running maximum, in log2 units: weights
+// are at most 2^8 against the maximum (it may lag by 8) and there are 2^4 in each of the item's
+// tiles, so their sum stays below 1 and a weighted sum of values within the values' own range
+// (with weights near 1 a value of 1e36 overflowed). It costs range at the other end: weights
+// below 2^-80 of the largest, 2^30 tokens taken, are 0.
+__device__ __forceinline__ float pat_above(int tiles) { return 12.f + (32 - __clz(tiles)); }
+
+// The natural logarithm of l 2^m (l = 0: no visible key), m a score in the units of scale_log2 plus
+// `above` in units of log 2 itself. With l = f 2^e the large parts of m and log l cancel in m + e.
+__device__ __forceinline__ float pat_lse(const PagedAttnArgs& a, float m, float l, float above) {
+  if (l == 0.f) return -INFINITY;
+  const int e = (int)(__float_as_uint(l) >> 23) - 126;  // l > 0 is far above the subnormal numbers, or NaN
+  const float f = l * __uint_as_float((uint32_t)(127 - e) << 23);
+  m += e;
+  return fmaf(m, a.ln_hi, fmaf(m, a.ln_lo, fmaf(above + e, a.ln_off, logf(f))));
 }
 
 // Work split. A call has one item per (sequence, key head, tile of up to QR query heads of
@@ -415,6 +427,7 @@ struct PatWarp;
 // other sign; where the first half is infinite or NaN, it is the result.
 // The running maximum moves only when a tile exceeds it by more than 8 (weights and sums against
 // an older maximum are at most 2^8 larger, and as exact), so most tiles do not rescale the output.
+// What is kept as the maximum lies above it by pat_above of the item's tiles.
 template <int HD, int QR>
 struct PatWarp<bf16, HD, QR> {
   using S = PatShape<bf16, HD, QR>;
@@ -423,10 +436,11 @@ struct PatWarp<bf16, HD, QR> {
   uint32_t qf[KS][2 * RV];
   float acc[NT][4];  // QR 8: [2], [3] for the remainders
   float rest[NT][4];  // QR 16: the remainders'
-  float m[RV], l[RV];
+  float m[RV], l[RV], lag;
 
   __device__ __forceinline__ void init(char*) {}
-  __device__ __forceinline__ void begin(const char* q, int rows, int lane) {
+  __device__ __forceinline__ void begin(const char* q, int rows, int tiles, int lane) {
+    lag = pat_above(tiles) - 8.f;
     const uint32_t qs = smem_u32(q);
     // rows 0..7 (and 8..15) of Q as first-operand fragments; rows that do not exist repeat row 0
     // and are not written
@@ -499,12 +513,12 @@ struct PatWarp<bf16, HD, QR> {
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
       mx[r] = t;
-      move |= t > m[r] + 8.f;
+      move |= t + lag > m[r];
     }
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
       for (int r = 0; r < RV; ++r) {
-        const float mn = fmaxf(m[r], mx[r]);
+        const float mn = fmaxf(m[r], mx[r] + (lag + 8.f));
         const float f = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
         m[r] = mn;
         l[r] *= f;
@@ -586,7 +600,7 @@ struct PatWarp<float, HD, QR> {
   using S = PatShape<float, HD, QR>;
   static constexpr int CPR = HD / 4, E = HD / 32;
   float acc[QR][E];
-  float m[QR], l[QR];
+  float m[QR], l[QR], lag;
   float4* qb;  // [QR][CPR]
   float* wb;   // [QR][PAT_TILE]
 
@@ -594,7 +608,8 @@ struct PatWarp<float, HD, QR> {
     qb = reinterpret_cast<float4*>(side);
     wb = reinterpret_cast<float*>(side + QR * HD * 4);
   }
-  __device__ __forceinline__ void begin(const char* qs, int rows, int lane) {
+  __device__ __forceinline__ void begin(const char* qs, int rows, int tiles, int lane) {
+    lag = pat_above(tiles) - 8.f;
     // the stage is refilled before the item ends
     const float4* from = reinterpret_cast<const float4*>(qs);
     for (int i = lane; i < QR * CPR; i += 32)
@@ -631,8 +646,8 @@ struct PatWarp<float, HD, QR> {
       s[r] = seen ? s[r] * scale_log2 : -INFINITY;
       // as above, the maximum moves only when a score exceeds it by more than 8; most tiles need
       // one vote per row and no reduction
-      if (__any_sync(0xffffffffu, s[r] > m[r] + 8.f)) {
-        float t = fmaxf(m[r], s[r]);
+      if (__any_sync(0xffffffffu, s[r] + lag > m[r])) {
+        float t = fmaxf(m[r], s[r] + (lag + 8.f));
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
         const float f = exp2f(m[r] - t);
@@ -698,13 +713,14 @@ struct PatOut {
   float* part;  // row 0 of the piece
   float2* ml;
   int hd;
+  float above;
   __device__ __forceinline__ float stat(int row, float m, float l, bool first) const {
     if (!out) {
       if (first) ml[row] = make_float2(m, l);
       return 1.f;
     }
     // l is 0 when every page id was bad
-    if (first && lse) lse[row] = pat_lse(a, m, l);
+    if (first && lse) lse[row] = pat_lse(a, m, l, above);
     return l == 0.f ? 0.f : 1.f / l;
   }
   __device__ __forceinline__ void pair(int row, int d, float x, float y) const {
@@ -748,8 +764,8 @@ struct PatSum {
   }
   // to `to`, and the logarithm of the sum to lse (nullable)
   template <class T>
-  __device__ __forceinline__ void store(const PagedAttnArgs& a, T* to, float* lse) const {
-    if (lse) *lse = pat_lse(a, m, l);
+  __device__ __forceinline__ void store(const PagedAttnArgs& a, T* to, float* lse, int tiles) const {
+    if (lse) *lse = pat_lse(a, m, l, pat_above(tiles));
     const float f = l == 0.f ? 0.f : 1.f / l;
     if constexpr (sizeof(T) == 2)
       *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
@@ -764,8 +780,8 @@ struct PatSum {
 // `rounds` rounds; `scratch` has 24 bytes per thread.
 constexpr int PAJ_AHEAD = 8;
 template <class T, int HD>
-__device__ __forceinline__ void pat_join(const PagedAttnArgs& a, const PagedAttnPlan& pl, int c0, int c1, int rows, T* out, float* lse,
-                                         char* scratch, int t, int threads, int rounds) {
+__device__ __forceinline__ void pat_join(const PagedAttnArgs& a, const PagedAttnPlan& pl, int c0, int c1, int rows, int tiles, T* out,
+                                         float* lse, char* scratch, int t, int threads, int rounds) {
   constexpr int VEC = HD / 4;
   float4* s_o = reinterpret_cast<float4*>(scratch);
   float2* s_ml = reinterpret_cast<float2*>(scratch + 16 * blockDim.x);
@@ -804,7 +820,7 @@ __device__ __forceinline__ void pat_join(const PagedAttnArgs& a, const PagedAttn
         const float4 x[1] = {s_o[threadIdx.x + i * cols]};
         sum.add(ml, x);
       }
-      sum.store(a, out + row * HD + v * 4, lse && v == 0 ? lse + row : nullptr);
+      sum.store(a, out + row * HD + v * 4, lse && v == 0 ? lse + row : nullptr, tiles);
     }
     __syncthreads();
   }
@@ -824,6 +840,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR, HP>::MAX_WARPS * 32, 1)
   // worker, [1 + warp] the one that begins in a warp and does not end there (seq < 0: none)
   struct Split {
     int seq, h, rows;    // its query heads
+    int tiles;
     int b0, b1, p0, p1;  // its blocks, and the warps of this block that have a piece of it
   };
   __shared__ Split s_split[S::MAX_WARPS + 1];
@@ -1032,7 +1049,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR, HP>::MAX_WARPS * 32, 1)
       if (t == 0 || c.tile == 0) {
 #pragma unroll
         for (int i = 0; i < HP; ++i)
-          pw[i].begin(ring + S::RING + (stage * pl.rows + i * pl.group) * S::ROW, HP == 1 ? pl.rows : pl.group, lane);
+          pw[i].begin(ring + S::RING + (stage * pl.rows + i * pl.group) * S::ROW, HP == 1 ? pl.rows : pl.group, c.tiles, lane);
         from = c.tile;
       }
 #pragma unroll
@@ -1061,12 +1078,13 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR, HP>::MAX_WARPS * 32, 1)
           out.part = reinterpret_cast<float*>(piece) + r0 * HD;
           out.ml = reinterpret_cast<float2*>(piece + pl.rows * HD * 4) + r0;
           out.hd = HD;
+          out.above = pat_above(c.tiles);
           pw[i].finish(lane, out);
         }
         if (!whole && lane == 0 && (from == 0 || warp == 0)) {
           const int64_t start = u0 + t - c.tile, last = start + c.tiles - 1;  // the item's first and last tile
           const int k = from == 0 ? warp + 1 : 0;
-          Split sp{c.seq, h, rows, (int)blockIdx.x, (int)blockIdx.x, from == 0 ? warp : 0, pl.warps - 1};
+          Split sp{c.seq, h, rows, c.tiles, (int)blockIdx.x, (int)blockIdx.x, from == 0 ? warp : 0, pl.warps - 1};
           if (last < a1) sp.p1 = (int)paged_div(last - a0, share);
           if (k == 0) sp.b0 = (int)paged_div(start, range);
           if (last >= a1) sp.b1 = (int)paged_div(last, range);
@@ -1113,7 +1131,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR, HP>::MAX_WARPS * 32, 1)
     }
     if (k > 0 && sp.b1 == (int)blockIdx.x) {
       sum.store(a, static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD + col * 4,
-                a.lse && v == 0 ? a.lse + (int64_t)sp.seq * a.nh + sp.h + row : nullptr);
+                a.lse && v == 0 ? a.lse + (int64_t)sp.seq * a.nh + sp.h + row : nullptr, sp.tiles);
     } else {
       const int64_t slot = ((int64_t)blockIdx.x * 2 + (k > 0 ? 1 : 0)) * pl.rows;
       reinterpret_cast<float4*>(pl.part + slot * HD)[col] = sum.o;
@@ -1143,7 +1161,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR, HP>::MAX_WARPS * 32, 1)
   const int threads = both ? blockDim.x / 2 : blockDim.x;
   const int i = both ? (int)threadIdx.x >= threads : !s_last[0];
   const Split sp = s_split[s_cross[i]];
-  pat_join<T, HD>(a, pl, sp.b0, sp.b1, sp.rows, static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD,
+  pat_join<T, HD>(a, pl, sp.b0, sp.b1, sp.rows, sp.tiles, static_cast<T*>(a.out) + sp.seq * a.ldo + sp.h * HD,
                   a.lse ? a.lse + (int64_t)sp.seq * a.nh + sp.h : nullptr, pat_smem, threadIdx.x - (both ? i * threads : 0),
                   threads, (cols + threads - 1) / threads);
 }
