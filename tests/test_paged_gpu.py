@@ -452,6 +452,25 @@ def test_attention_is_deterministic_on_a_used_workspace(dtype):
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("NH,nkv", [(40, 2), (20, 1), (17, 1), (11, 1), (5, 5), (3, 3)])
+@pytest.mark.parametrize("hd", [32, 64, 128])
+def test_attention_does_not_depend_on_what_ran_before(dtype, NH, nkv, hd):
+    # groups that are no multiple of a query tile: rows of the tile that do not exist
+    lens = [3000, 10, 700, 1, 64, 129, 333, 1500]
+    kv, q, ln, out, lse, _ = attention_case(lens, NH, nkv, hd, 16, dtype, "heads", seed=81)
+    most = torch.full_like(ln, 3000 - 3000 % 16)
+    other = tsb.PagedKV(*(torch.randn(200, 16, 1, hd, device="cuda").to(dtype) for _ in range(2)),
+                        torch.arange(200, dtype=torch.int32, device="cuda").repeat(len(lens), 1))
+    for x in (0.0, 30.0, -30.0, 1e4, math.nan):
+        # large queries of every row of the tile in all of the SMs' shared memory
+        big = (torch.randn(len(lens), 32, hd, device="cuda") * x).to(dtype)
+        tsb.paged_attention(other, big, most, torch.empty_like(big))
+        got, l2 = torch.empty_like(out), torch.empty_like(lse)
+        tsb.paged_attention(kv, q, ln, got, lse=l2)
+        assert torch.equal(l2, lse) and torch.equal(got, out)
+
+
 # ---------------------------------------------------------------------------
 # append
 # ---------------------------------------------------------------------------

@@ -1047,9 +1047,11 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR, HP>::MAX_WARPS * 32, 1)
         __syncwarp();
       }
       if (t == 0 || c.tile == 0) {
+        // the rows that have arrived: what the others' places hold must not count in the warp's votes
+        const int rows = HP > 1 || pl.qtiles == 1 ? pl.rows / HP : min(QR, pl.group - c.item % pl.qtiles * QR);
 #pragma unroll
         for (int i = 0; i < HP; ++i)
-          pw[i].begin(ring + S::RING + (stage * pl.rows + i * pl.group) * S::ROW, HP == 1 ? pl.rows : pl.group, c.tiles, lane);
+          pw[i].begin(ring + S::RING + (stage * pl.rows + i * pl.group) * S::ROW, rows, c.tiles, lane);
         from = c.tile;
       }
 #pragma unroll
