@@ -807,3 +807,35 @@ def test_calls_on_other_streams():
     torch.cuda.synchronize()
     for o in outs + [own]:
         assert torch.equal(o, out)
+
+
+def small_cache():
+    kc, vc = (torch.zeros(8, 4, 2, 32, device="cuda") for _ in range(2))
+    return tsb.PagedKV(kc, vc, torch.arange(8, dtype=torch.int32).view(4, 2).cuda())
+
+
+def raises_page_range(kv, stream=None):
+    try:
+        kv.check(stream)
+    except tsb.Gpt2Error as e:
+        assert e.code == -9
+        return True
+    return False
+
+
+def test_no_report_is_lost_between_streams():
+    # a call on one stream meets a bad position while the word is read and cleared on another:
+    # that check or the next one reports it
+    kv = small_cache()
+    k = torch.ones(1, 2, 32, device="cuda")
+    pos = torch.tensor([8], dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    kv.check()
+    for i in range(3000):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(97 * (i % 300))  # up to some 15 us
+            tsb.paged_kv_append(kv, k, k, pos)
+        first = raises_page_range(kv)
+        side.synchronize()
+        assert raises_page_range(kv) or first, i

@@ -1558,14 +1558,10 @@ int gpt2_op_paged_status(const gpt2_paged_kv* kv, void* stream) {
     return GPT2_ERR_CONFIG;
   }
   OpCtx o(stream);
-  int h = 0;
-  cudaError_t e = cudaMemcpyAsync(&h, kv->status, sizeof(int), cudaMemcpyDeviceToHost, o.s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(kv->status, 0, sizeof(int), o.s);
-  if (e != cudaSuccess) {
-    g_op_error = std::string("paged_status: ") + cudaGetErrorString(e);
-    return GPT2_ERR_CUDA;
-  }
-  return OpCtx::sync_and_translate(o.s, h);
+  RK(o.alloc_err());
+  const int r = paged_take_status(o.c, kv->status, o.d_err);
+  const int r2 = o.finish();
+  return r ? r : r2;
 }
 
 int gpt2_op_bounded_wait_check(int arrive, unsigned long long limit_ns, void* stream) {

@@ -1177,6 +1177,11 @@ inline int paged_view(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedView* ou
   return GPT2_OK;
 }
 
+inline int paged_take_status(const LaunchCtx& c, int* status, int* out) {
+  paged_take_status_kernel<<<1, 1, 0, c.stream>>>(status, out);
+  return check_launch(c, "paged_status");
+}
+
 // rows of `heads` heads: base and row stride on 16 bytes, rows that do not overlap
 inline bool paged_rows_ok(const void* p, int64_t ld, int64_t heads, int hd, int64_t vn) {
   return p && !(reinterpret_cast<uintptr_t>(p) & 15) && ld % vn == 0 && ld >= heads * hd;

@@ -30,6 +30,10 @@ __device__ __forceinline__ int paged_page(const PagedView& c, int seq, int pos) 
   return (unsigned)page < (unsigned)c.n_pages ? page : -1;
 }
 
+// The status word, cleared: in one step, so that what a call on another stream raises meanwhile is
+// reported now or the next time.
+__global__ void paged_take_status_kernel(int* status, int* out) { *out = atomicExch(status, 0); }
+
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
