@@ -442,8 +442,8 @@ int gpt2_op_sample_topk(const float* logits, int64_t ld, int rows, int V, int k,
  * (GPT2_ERR_CONFIG, _BATCH or _SEQ_TOO_LONG otherwise, before anything is launched).
  * status (nullable): int32 device word, zero at first. Contents of device memory cannot be
  * checked by the host: a page id outside [0, n_pages), a sequence, position or length outside
- * the cache is not followed, the access is skipped as documented at each call, and the word
- * is raised (as it is by a bounded wait that gave up); gpt2_op_paged_status reports it.
+ * the cache is not followed, the access is skipped as documented at each call, and bit 0 of the
+ * word is set (bit 1 by a bounded wait that gave up); gpt2_op_paged_status reports it.
  * The struct is read during the call only. */
 typedef struct {
   void *k, *v;
@@ -518,7 +518,8 @@ size_t gpt2_paged_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, 
 
 /* Wait for `stream`, read and clear the cache's status word: GPT2_ERR_PAGE_RANGE if a call on
  * the cache met a bad page id, sequence, position or length since it was last cleared,
- * GPT2_ERR_TIMEOUT if a wait gave up (its results are void). GPT2_ERR_CONFIG for a cache
+ * GPT2_ERR_TIMEOUT, whether or not one did, if a wait gave up (its results are void). What calls
+ * on other streams raise meanwhile is reported now or the next time. GPT2_ERR_CONFIG for a cache
  * without one. */
 int gpt2_op_paged_status(const gpt2_paged_kv* kv, void* stream);
 

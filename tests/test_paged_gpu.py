@@ -839,3 +839,21 @@ def test_no_report_is_lost_between_streams():
         first = raises_page_range(kv)
         side.synchronize()
         assert raises_page_range(kv) or first, i
+
+
+def test_a_wait_that_gave_up_is_reported_before_a_bad_page():
+    # the word as the header describes it: 1 for something outside the cache, 2 for a wait that
+    # gave up (after which the results are void, whatever else was met)
+    kv = small_cache()
+    for word, code in ((1, -9), (2, -8), (3, -8)):
+        kv.status.fill_(word)
+        with pytest.raises(tsb.Gpt2Error) as e:
+            kv.check()
+        assert e.value.code == code
+        kv.check()
+    k = torch.ones(1, 2, 32, device="cuda")
+    kv.status.fill_(2)
+    tsb.paged_kv_append(kv, k, k, torch.tensor([8], dtype=torch.int32, device="cuda"))
+    with pytest.raises(tsb.Gpt2Error) as e:
+        kv.check()
+    assert e.value.code == -8

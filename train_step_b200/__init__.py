@@ -655,8 +655,9 @@ class PagedKV:
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def check(self, stream=None) -> None:
-        """Wait for the stream and raise Gpt2Error(GPT2_ERR_PAGE_RANGE) if a call on this cache
-        met a bad page id, sequence, position or length since the last check."""
+        """Wait for the stream and raise Gpt2Error if a call on this cache met a bad page id,
+        sequence, position or length since the last check (GPT2_ERR_PAGE_RANGE) or gave up waiting
+        for a copy (GPT2_ERR_TIMEOUT: results are void)."""
         with _device_of(self._index):
             _op(lib().gpt2_op_paged_status(self._ref, self._current_stream(self._index) if stream is None else stream))
 

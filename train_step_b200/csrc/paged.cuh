@@ -30,9 +30,20 @@ __device__ __forceinline__ int paged_page(const PagedView& c, int seq, int pos) 
   return (unsigned)page < (unsigned)c.n_pages ? page : -1;
 }
 
-// The status word, cleared: in one step, so that what a call on another stream raises meanwhile is
-// reported now or the next time.
-__global__ void paged_take_status_kernel(int* status, int* out) { *out = atomicExch(status, 0); }
+// Bits of the status word, set by kernels.
+constexpr int PAGED_OUTSIDE = 1;  // a page id, sequence, position or length outside the cache
+constexpr int PAGED_TIMEOUT = 2;  // a bounded wait gave up: results are void, whatever else was met
+
+__device__ __forceinline__ void raise_paged_status(int* status, int bit) {
+  if (status) atomicOr(status, bit);
+}
+
+// The status word as an error code, and cleared: in one step, so that what a call on another stream
+// raises meanwhile is reported now or the next time.
+__global__ void paged_take_status_kernel(int* status, int* out) {
+  const int word = atomicExch(status, 0);
+  *out = word & PAGED_TIMEOUT ? DEV_TIMEOUT : word & PAGED_OUTSIDE ? DEV_PAGE_RANGE : DEV_OK;
+}
 
 // ---------------------------------------------------------------------------
 // append
@@ -128,7 +139,7 @@ __global__ void __launch_bounds__(PKV_THREADS, PKV_BLOCKS) paged_append_kernel(c
         (a.rot == 0 || pos < a.n_positions))
       page = paged_page(a.c, seq, pos);
     if (page < 0) {
-      raise_device_error(a.c.status, DEV_PAGE_RANGE);
+      raise_paged_status(a.c.status, PAGED_OUTSIDE);
       continue;
     }
     if (cached) dst += page * a.c.page_stride + (pos & ((1 << a.c.log2_page) - 1)) * a.c.row_stride + head;
@@ -342,7 +353,7 @@ __device__ __forceinline__ int pat_prefix(const PagedAttnArgs& a, int* before) {
       n = paged_length(a.lens[lane], a.c.max_pages << a.c.log2_page, &bad);
       n = paged_visible(n, a.window, a.sinks).tiles;
     }
-    if (bad && blockIdx.x == 0 && threadIdx.x < 32) raise_device_error(a.c.status, DEV_PAGE_RANGE);
+    if (bad && blockIdx.x == 0 && threadIdx.x < 32) raise_paged_status(a.c.status, PAGED_OUTSIDE);
     const int most = __reduce_max_sync(0xffffffffu, n);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -367,7 +378,7 @@ __device__ __forceinline__ int pat_prefix(const PagedAttnArgs& a, int* before) {
     most = max(most, n);
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  if (bad && blockIdx.x == 0) raise_device_error(a.c.status, DEV_PAGE_RANGE);
+  if (bad && blockIdx.x == 0) raise_paged_status(a.c.status, PAGED_OUTSIDE);
   int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -1105,7 +1116,7 @@ __global__ void __launch_bounds__(PatShape<T, HD, QR, HP>::MAX_WARPS * 32, 1)
       }
     }
     if (!BOX) cp_async_wait<0>();
-    if (bad) raise_device_error(a.c.status, bad == 2 ? DEV_TIMEOUT : DEV_PAGE_RANGE);
+    if (bad) raise_paged_status(a.c.status, bad == 2 ? PAGED_TIMEOUT : PAGED_OUTSIDE);
   }
   __syncthreads();
   // a thread joins four elements of a split item's row over the block's pieces
