@@ -857,3 +857,20 @@ def test_a_wait_that_gave_up_is_reported_before_a_bad_page():
     with pytest.raises(tsb.Gpt2Error) as e:
         kv.check()
     assert e.value.code == -8
+
+
+def test_a_cache_is_ready_for_every_stream():
+    # the status word is set up behind other work on the constructor's stream; a call on another
+    # stream does not wait for that, and its report must last
+    k = torch.ones(1, 2, 32, device="cuda")
+    pos = torch.tensor([8], dtype=torch.int32, device="cuda")
+    kc, vc = (torch.zeros(8, 4, 2, 32, device="cuda") for _ in range(2))
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(4, 2)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    kv = tsb.PagedKV(kc, vc, table)
+    tsb.paged_kv_append(kv, k, k, pos, stream=side.cuda_stream)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert raises_page_range(kv)

@@ -634,6 +634,9 @@ class PagedKV:
         n_pages, page_size, self.n_kv_heads, self.head_dim = k_cache.shape
         self.n_seqs, max_pages = page_table.shape
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        with torch.cuda.device(self.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()  # the word is set before a call on any stream
         ps, rs, hs, _ = k_cache.stride()
         # a table of one row may have any stride, and so may a dimension of one element
         ts = page_table.stride(0) if self.n_seqs > 1 else max_pages
