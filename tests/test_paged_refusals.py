@@ -268,3 +268,56 @@ def test_binding_refuses_what_is_not_on_a_gpu():
     k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         tsb.PagedKV(k, k.clone(), torch.zeros(2, 2, dtype=torch.int32))
+
+
+GUARD_CHECK = r"""
+#include <dlfcn.h>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <new>
+#include "gpt2.h"
+// the library's allocations come here, and fail when `full`
+static bool full = false;
+void* operator new(std::size_t n) {
+  void* p = full ? nullptr : std::malloc(n);
+  if (!p) throw std::bad_alloc();
+  return p;
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, std::size_t) noexcept { std::free(p); }
+int main(int, char** argv) {
+  void* lib = dlopen(argv[1], RTLD_NOW);
+  if (!lib) return std::printf("%s\n", dlerror()), 1;
+  auto append = (decltype(&gpt2_op_paged_kv_append))dlsym(lib, "gpt2_op_paged_kv_append");
+  auto attend = (decltype(&gpt2_op_paged_attention))dlsym(lib, "gpt2_op_paged_attention");
+  auto status = (decltype(&gpt2_op_paged_status))dlsym(lib, "gpt2_op_paged_status");
+  auto error = (decltype(&gpt2_op_last_error))dlsym(lib, "gpt2_op_last_error");
+  // in each case the message of the refusal, then the same without memory for it
+  for (int i = 0; i < 3; ++i) {
+    auto call = [&] { return i == 0 ? append(nullptr, nullptr, nullptr) : i == 1 ? attend(nullptr, nullptr, nullptr)
+                                                                                  : status(nullptr, nullptr); };
+    full = true;  // first, while no string has memory from before
+    const int none = call();
+    full = false;
+    if (i < 2 && (none != GPT2_ERR_OOM || !std::strstr(error(), "memory"))) return 10 + i;
+    if (i == 2 && none != GPT2_ERR_OOM && none != GPT2_ERR_CONFIG) return 12;
+    if (call() != GPT2_ERR_CONFIG || !std::strstr(error(), "paged")) return 20 + i;
+    full = true;
+    const int again = call();
+    full = false;
+    if (again == GPT2_ERR_OOM ? !std::strstr(error(), "memory") : again != GPT2_ERR_CONFIG) return 30 + i;
+  }
+  return 0;
+}
+"""
+
+
+def test_host_memory_that_runs_out_is_reported_as_that(tmp_path):
+    # no exception leaves the library, and the message is that of the failure, not of an earlier one
+    src, exe = tmp_path / "guard.cpp", tmp_path / "guard"
+    src.write_text(GUARD_CHECK)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-rdynamic", "-I" + os.path.join(ROOT, "include"), str(src), "-o",
+                    str(exe), "-ldl"], check=True)
+    got = subprocess.run([str(exe), tsb.LIB_PATH], capture_output=True, text=True, timeout=60)
+    assert got.returncode == 0, (got.returncode, got.stdout, got.stderr)

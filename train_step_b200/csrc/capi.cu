@@ -7,6 +7,7 @@
 #include <string>
 #include <vector>
 
+#include "guard.cuh"
 #include "launch.cuh"
 
 using namespace g2;
@@ -30,16 +31,6 @@ struct LayerP {
 };
 
 thread_local std::string g_op_error;
-
-// f(), with no exception (host memory that ran out) across the C boundary
-template <class F>
-int guarded(F&& f) {
-  try {
-    return f();
-  } catch (...) {
-    return GPT2_ERR_OOM;
-  }
-}
 
 uint64_t splitmix64_at(uint64_t x) {
   uint64_t z = x + 0x9E3779B97F4A7C15ull;
@@ -1541,7 +1532,7 @@ int gpt2_op_sample_topk(const float* logits, int64_t ld, int rows, int V, int k,
 }
 
 int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const gpt2_paged_rows* rows, void* stream) {
-  return guarded([&] { return paged_kv_append(OpCtx(stream).c, kv, rows); });
+  return guarded(&g_op_error, [&] { return paged_kv_append(OpCtx(stream).c, kv, rows); });
 }
 
 size_t gpt2_paged_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int head_dim) {
@@ -1549,19 +1540,24 @@ size_t gpt2_paged_attention_ws_bytes(int n_seqs, int n_q_heads, int n_kv_heads, 
 }
 
 int gpt2_op_paged_attention(const gpt2_paged_kv* kv, const gpt2_paged_query* query, void* stream) {
-  return guarded([&] { return paged_attention(OpCtx(stream).c, kv, query); });
+  return guarded(&g_op_error, [&] { return paged_attention(OpCtx(stream).c, kv, query); });
 }
 
 int gpt2_op_paged_status(const gpt2_paged_kv* kv, void* stream) {
-  if (!kv || !kv->status) {
-    g_op_error = "paged_status: the cache has no status word";
-    return GPT2_ERR_CONFIG;
-  }
-  OpCtx o(stream);
-  RK(o.alloc_err());
-  const int r = paged_take_status(o.c, kv->status, o.d_err);
-  const int r2 = o.finish();
-  return r ? r : r2;
+  return guarded(&g_op_error, [&]() -> int {
+    if (!kv || !kv->status) {
+      g_op_error = "paged_status: the cache has no status word";
+      return GPT2_ERR_CONFIG;
+    }
+    OpCtx o(stream);
+    if (o.alloc_err()) {
+      g_op_error = "paged_status: no device memory";
+      return GPT2_ERR_OOM;
+    }
+    const int r = paged_take_status(o.c, kv->status, o.d_err);
+    const int r2 = o.finish();
+    return r ? r : r2;
+  });
 }
 
 int gpt2_op_bounded_wait_check(int arrive, unsigned long long limit_ns, void* stream) {
