@@ -321,3 +321,9 @@ def test_host_memory_that_runs_out_is_reported_as_that(tmp_path):
                     str(exe), "-ldl"], check=True)
     got = subprocess.run([str(exe), tsb.LIB_PATH], capture_output=True, text=True, timeout=60)
     assert got.returncode == 0, (got.returncode, got.stdout, got.stderr)
+
+
+def test_status_refuses_a_misaligned_word():
+    for at in (1, 2, 3):
+        assert tsb.lib().gpt2_op_paged_status(ct.byref(cache(status=A + at)), None) == CONFIG
+        assert b"aligned" in tsb.lib().gpt2_op_last_error()

@@ -1549,6 +1549,10 @@ int gpt2_op_paged_status(const gpt2_paged_kv* kv, void* stream) {
       g_op_error = "paged_status: the cache has no status word";
       return GPT2_ERR_CONFIG;
     }
+    if (reinterpret_cast<uintptr_t>(kv->status) & 3) {
+      g_op_error = "paged_status: the status word must be 4-byte aligned";
+      return GPT2_ERR_CONFIG;
+    }
     OpCtx o(stream);
     if (o.alloc_err()) {
       g_op_error = "paged_status: no device memory";
