@@ -463,7 +463,8 @@ typedef struct {
  * 2i + 1) when interleaved != 0, becomes (x c_i - y s_i, x s_i + y c_i), computed in fp32 and
  * rounded once; elements from rot_dim on are copied. q (nullable, with q_out and n_q_heads):
  * query rows of the same tokens, rotated the same way into q_out (may be q itself, with the
- * same row stride, but not overlap it otherwise). A row whose position, sequence, table entry or
+ * same row stride; GPT2_ERR_CONFIG when its rows overlap those of q, k or v otherwise; it may not
+ * overlap the cache either). A row whose position, sequence, table entry or
  * rotation row is outside its range is skipped and raises the status word; rows that are skipped
  * leave q_out as it was. Rows must name distinct slots: of two rows for one slot, each 16 bytes
  * come from either. The cache's strides must keep its heads apart, each stepping over what the

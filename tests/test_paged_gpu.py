@@ -874,3 +874,24 @@ def test_a_cache_is_ready_for_every_stream():
     side.synchronize()
     torch.cuda.synchronize()
     assert raises_page_range(kv)
+
+
+def test_append_into_rows_between_others():
+    # queries, keys, values and the rotated queries side by side in one tensor's rows
+    g = torch.Generator().manual_seed(91)
+    for dtype in BOTH:
+        kc, vc = (torch.zeros(8, 4, 2, 32, dtype=dtype, device="cuda") for _ in range(2))
+        kv = tsb.PagedKV(kc, vc, torch.arange(8, dtype=torch.int32).view(4, 2).cuda())
+        rows = torch.randn(4, 12, 32, generator=g).to(dtype).cuda()
+        pos = torch.tensor([6, 0, -1, 3], dtype=torch.int32, device="cuda")
+        cs, was = tsb.rotation_table(8, 32), rows.clone()
+        own = torch.full((4, 4, 32), 3.0, dtype=dtype, device="cuda")
+        tsb.paged_kv_append(kv, rows[:, 4:6], rows[:, 6:8], pos, q=rows[:, :4], q_out=own, cos_sin=cs)
+        tsb.paged_kv_append(kv, rows[:, 4:6], rows[:, 6:8], pos, q=rows[:, :4], q_out=rows[:, 8:], cos_sin=cs)
+        kv.check()
+        live = pos >= 0
+        assert torch.equal(rows[:, :8], was[:, :8]) and torch.equal(rows[live][:, 8:], own[live])
+        assert torch.equal(rows[2, 8:], was[2, 8:])
+        for bad in (rows[:, 1:5], rows[:, 7:11]):
+            with pytest.raises(tsb.Gpt2Error):
+                tsb.paged_kv_append(kv, rows[:, 4:6], rows[:, 6:8], pos, q=rows[:, :4], q_out=bad, cos_sin=cs)

@@ -327,3 +327,52 @@ def test_status_refuses_a_misaligned_word():
     for at in (1, 2, 3):
         assert tsb.lib().gpt2_op_paged_status(ct.byref(cache(status=A + at)), None) == CONFIG
         assert b"aligned" in tsb.lib().gpt2_op_last_error()
+
+
+@pytest.mark.parametrize("change", [
+    dict(q_out=A, ldqo=264), dict(q_out=A, ldqo=512), dict(q_out=A, ldq=264), dict(q_out=A + 16), dict(q_out=A + 512),
+    dict(q=A + 512), dict(q=A + 1040, ldq=512, q_out=A, ldqo=520), dict(q_out=A, ldqo=768, ldq=768, k=A + 496, ldk=768),
+    dict(q=A + 8192, ldq=512, k=A + 512, ldk=512, v=A + 784, ldv=512, q_out=A, ldqo=512, N=2)])
+def test_append_refuses_overlapping_query_rows(change):
+    # (elements are 2 bytes; a row of 4 query heads has 512, one of 2 key heads 256)
+    f = dict(k=A + (1 << 20), v=A + (2 << 20))
+    f.update(change)
+    assert append(cache(), **f) == CONFIG
+    assert b"q_out" in tsb.lib().gpt2_op_last_error()
+
+
+APART_CHECK = r"""
+#include <set>
+#include "paged_index.cuh"
+using namespace g2;
+int main() {
+  for (int n = 1; n <= 4; ++n)
+    for (int wa = 1; wa <= 3; ++wa)
+      for (int wb = 1; wb <= 3; ++wb)
+        for (int lda = wa; lda <= 8; ++lda)
+          for (int ldb = wb; ldb <= 8; ++ldb)
+            for (int d = -36; d <= 36; ++d) {
+              bool apart = true, in_place = true;
+              for (int i = 0; i < n; ++i)
+                for (int j = 0; j < n; ++j) {
+                  const int a = i * lda, b = d + j * ldb;
+                  if (a + wa <= b || b + wb <= a) continue;
+                  apart = false;
+                  if (i != j || a != b || wa != wb) in_place = false;
+                }
+              if (paged_rows_apart(lda, wa, d, ldb, wb, n, false) != apart) return 1;
+              if (paged_rows_apart(lda, wa, d, ldb, wb, n, true) != in_place) return 2;
+            }
+  const int64_t far = INT64_MAX / 2;  // strides that overflow 64 bits when they are multiplied out
+  if (!paged_rows_apart(far, 64, 64, far, 64, 1 << 20, false) || paged_rows_apart(far, 64, 32, far, 64, 1 << 20, true)) return 3;
+  return 0;
+}
+"""
+
+
+def test_overlap_of_rows(tmp_path):
+    src, exe = tmp_path / "apart.cpp", tmp_path / "apart"
+    src.write_text(APART_CHECK)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-I" + os.path.join(ROOT, "train_step_b200", "csrc"), str(src), "-o",
+                    str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0

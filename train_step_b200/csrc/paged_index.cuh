@@ -104,4 +104,31 @@ G2_HD bool paged_next(PagedCursor& c, const int* before, int items) {
   return true;
 }
 
+// n rows of `wa` bytes at 0, lda, 2 lda ... and n of `wb` bytes at d, d + ldb ... (host): whether no
+// byte belongs to a row of each. in_place: a row may also be the other's of the same index, exactly.
+inline bool paged_rows_apart(int64_t lda, int64_t wa, int64_t d, int64_t ldb, int64_t wb, int64_t n, bool in_place) {
+  typedef __int128 wide;
+  if (d >= (wide)lda * (n - 1) + wa || d + (wide)ldb * (n - 1) + wb <= 0) return true;
+  if (in_place && d == 0 && wa == wb && (lda == ldb || n == 1)) return true;
+  if (lda == ldb) {
+    // row i and row i + m of the other overlap when -wb < d + m ld < wa: two values of m can
+    int64_t m = -(d / lda), r = d % lda;
+    if (r < 0) r += lda, ++m;  // d + m ld = r
+    return !(r < wa && m > -n && m < n) && !(r > lda - wb && m - 1 > -n && m - 1 < n);
+  }
+  for (int64_t i = 0, j = 0; i < n && j < n;) {  // in the order of their places
+    const wide a = (wide)lda * i, b = d + (wide)ldb * j;
+    if (a + wa <= b) {
+      ++i;
+    } else if (b + wb <= a) {
+      ++j;
+    } else if (in_place && i == j && a == b && wa == wb) {
+      ++i, ++j;
+    } else {
+      return false;
+    }
+  }
+  return true;
+}
+
 }  // namespace g2
