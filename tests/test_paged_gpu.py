@@ -166,6 +166,37 @@ def test_attention_long_and_ragged(dtype, hd, NH, nkv):
 
 
 @pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("NH,nkv,hd,page,n", [(1, 1, 64, 16, 20000), (12, 12, 64, 16, 1024), (8, 1, 128, 64, 131071),
+                                              (16, 2, 64, 8, 9999), (6, 3, 32, 32, 30001), (5, 1, 96, 16, 7777)])
+def test_attention_counts_every_key_once(dtype, NH, nkv, hd, page, n):
+    """Equal scores (queries of zero): every weight is 1/n, the sum of exponentials is n, and an
+    output is the mean of a value that is 1 at some keys and 0 at the others. A tile of 16 keys
+    that is lost or counted twice moves the logarithm by 16/n. Weights are one power of two, sums
+    of them exact up to 2^24 of them, so the logarithm is off by its own roundings, 4 e (|log n| +
+    1) at most, and a mean c/n by those of the reciprocal and the product, 2 e, and one to T."""
+    assert n < 2 ** 24 and 16 / n > 64 * E * (math.log(n) + 1)
+    kc = torch.randn(-(-n // page) + 2, page, nkv, hd, device="cuda").to(dtype)
+    vc = torch.zeros_like(kc)
+    ids = torch.randperm(kc.shape[0], generator=torch.Generator().manual_seed(n))[:-(-n // page)].int()
+    t = torch.arange(n)
+    # element e: the keys of the tiles e, e + hd, e + 2 hd ...
+    flat = torch.zeros(ids.numel() * page, hd)
+    flat[t, (t // 16) % hd] = 1
+    vc[ids.long().cuda()] = flat.view(-1, page, 1, hd).to(dtype).cuda()
+    kv = tsb.PagedKV(kc, vc, ids[None].cuda())
+    q = torch.zeros(1, NH, hd, dtype=dtype, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(1, NH, device="cuda")
+    ws = kv.attention_workspace(NH)
+    for length in (n, n - 1, n - 15, n - 16, n - 17, n // 2 + 1):
+        tsb.paged_attention(kv, q, torch.tensor([length], dtype=torch.int32, device="cuda"), out, lse=lse, ws=ws)
+        count = torch.bincount((t[:length] // 16) % hd, minlength=hd).double()
+        assert ((lse.double().cpu() - math.log(length)).abs() <= 4 * E * (math.log(length) + 1)).all()
+        want = count / length
+        assert ((out.double().cpu() - want).abs() <= (unit(dtype) + 2 * E) * want).all()
+    kv.check()
+
+
+@pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("hd,NH,nkv,page", [(32, 6, 2, 16), (64, 16, 1, 8), (64, 40, 2, 16), (96, 9, 1, 64),
                                             (96, 5, 1, 4), (128, 16, 2, 32), (128, 12, 1, 16), (128, 3, 3, 2)])
 def test_attention_of_items_spread_over_blocks(dtype, hd, NH, nkv, page):
