@@ -1554,13 +1554,16 @@ int gpt2_op_paged_status(const gpt2_paged_kv* kv, void* stream) {
       return GPT2_ERR_CONFIG;
     }
     OpCtx o(stream);
-    if (o.alloc_err()) {
-      g_op_error = "paged_status: no device memory";
-      return GPT2_ERR_OOM;
+    int word = 0;
+    const cudaError_t e = cudaMemcpyAsync(&word, kv->status, sizeof(int), cudaMemcpyDeviceToHost, o.s);
+    if (e != cudaSuccess) {
+      g_op_error = std::string("paged_status: ") + cudaGetErrorString(e);
+      return GPT2_ERR_CUDA;
     }
-    const int r = paged_take_status(o.c, kv->status, o.d_err);
-    const int r2 = o.finish();
-    return r ? r : r2;
+    int r = OpCtx::sync_and_translate(o.s, DEV_OK);
+    if (r || !word) return r;
+    r = paged_clear_status(o.c, kv->status, word);
+    return r ? r : OpCtx::sync_and_translate(o.s, word & PAGED_TIMEOUT ? DEV_TIMEOUT : DEV_PAGE_RANGE);
   });
 }
 

@@ -1177,8 +1177,8 @@ inline int paged_view(const LaunchCtx& c, const gpt2_paged_kv* kv, PagedView* ou
   return GPT2_OK;
 }
 
-inline int paged_take_status(const LaunchCtx& c, int* status, int* out) {
-  paged_take_status_kernel<<<1, 1, 0, c.stream>>>(status, out);
+inline int paged_clear_status(const LaunchCtx& c, int* status, int bits) {
+  paged_clear_status_kernel<<<1, 1, 0, c.stream>>>(status, bits);
   return check_launch(c, "paged_status");
 }
 

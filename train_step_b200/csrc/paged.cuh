@@ -38,12 +38,9 @@ __device__ __forceinline__ void raise_paged_status(int* status, int bit) {
   if (status) atomicOr(status, bit);
 }
 
-// The status word as an error code, and cleared: in one step, so that what a call on another stream
-// raises meanwhile is reported now or the next time.
-__global__ void paged_take_status_kernel(int* status, int* out) {
-  const int word = atomicExch(status, 0);
-  *out = word & PAGED_TIMEOUT ? DEV_TIMEOUT : word & PAGED_OUTSIDE ? DEV_PAGE_RANGE : DEV_OK;
-}
+// Clears the bits that were read, so that one which a call on another stream sets meanwhile is
+// reported the next time.
+__global__ void paged_clear_status_kernel(int* status, int bits) { atomicAnd(status, ~bits); }
 
 // ---------------------------------------------------------------------------
 // append
