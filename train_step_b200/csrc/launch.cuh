@@ -1400,7 +1400,6 @@ inline int paged_attention(const LaunchCtx& c, const gpt2_paged_kv* kv, const gp
   const double ln = (double)scale / (double)a.scale_log2;
   a.ln_hi = (float)ln;
   a.ln_lo = (float)(ln - (double)a.ln_hi);
-  a.ln_off = (float)(0.69314718055994531 - ln);
   a.window = query->window;
   a.sinks = query->sinks;
   void* ws = query->ws;

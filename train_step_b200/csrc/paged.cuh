@@ -192,25 +192,23 @@ struct PagedAttnArgs {
   const int* lens;
   int window, sinks;
   // scale * log2 e, and scale divided by it (about ln 2) as a sum of two: maxima are held in log2
-  // units, and these give them back without the error of a rounded constant; log 2 less their sum too
-  float scale_log2, ln_hi, ln_lo, ln_off;
+  // units, and these give them back without the error of a rounded constant
+  float scale_log2, ln_hi, ln_lo;
 };
 
-// How far the reference of an item's weights lies above the running maximum, in log2 units: weights
-// are at most 2^8 against the maximum (it may lag by 8) and there are 2^4 in each of the item's
-// tiles, so their sum stays below 1 and a weighted sum of values within the values' own range
-// (with weights near 1 a value of 1e36 overflowed). It costs range at the other end: weights
-// below 2^-80 of the largest, 2^30 tokens taken, are 0.
-__device__ __forceinline__ float pat_above(int tiles) { return 12.f + (32 - __clz(tiles)); }
+// The weights 2^(s - m) of an item are multiplied by 2^-pat_above: they are at most 2^8 (the
+// maximum m may lag by 8) and there are 2^4 in each of the item's tiles, so their sum stays below 1
+// and a weighted sum of values within the values' own range (without it values of 1e36 overflowed).
+// (The same as an offset of m saves the product, but rounds the exponents of the weights that count:
+// fp32 outputs of 2,000 keys were off by 1.5e-7 for 0.9e-7, at the same speed.)
+__device__ __forceinline__ int pat_above(int tiles) { return 12 + (32 - __clz(tiles)); }
+__device__ __forceinline__ float pat_exp2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// The natural logarithm of l 2^m (l = 0: no visible key), m a score in the units of scale_log2 plus
-// `above` in units of log 2 itself. With l = f 2^e the large parts of m and log l cancel in m + e.
-__device__ __forceinline__ float pat_lse(const PagedAttnArgs& a, float m, float l, float above) {
+// The natural logarithm of l 2^(m + above), m in the units of scale_log2 (l = 0: no visible key).
+__device__ __forceinline__ float pat_lse(const PagedAttnArgs& a, float m, float l, int above) {
   if (l == 0.f) return -INFINITY;
   const int e = (int)(__float_as_uint(l) >> 23) - 126;  // l > 0 is far above the subnormal numbers, or NaN
-  const float f = l * __uint_as_float((uint32_t)(127 - e) << 23);
-  m += e;
-  return fmaf(m, a.ln_hi, fmaf(m, a.ln_lo, fmaf(above + e, a.ln_off, logf(f))));
+  return fmaf(m, a.ln_hi, fmaf(m, a.ln_lo, fmaf((float)(above + e), 0.69314718056f, logf(l * pat_exp2i(-e)))));
 }
 
 // Work split. A call has one item per (sequence, key head, tile of up to QR query heads of
@@ -439,20 +437,19 @@ struct PatWarp;
 // other sign; where the first half is infinite or NaN, it is the result.
 // The running maximum moves only when a tile exceeds it by more than 8 (weights and sums against
 // an older maximum are at most 2^8 larger, and as exact), so most tiles do not rescale the output.
-// What is kept as the maximum lies above it by pat_above of the item's tiles.
 template <int HD, int QR>
 struct PatWarp<bf16, HD, QR> {
   using S = PatShape<bf16, HD, QR>;
   static constexpr int KS = HD / 16, NT = HD / 8;
   static constexpr int RV = QR / 8;  // query rows a lane holds statistics of
   uint32_t qf[KS][2 * RV];
-  float acc[NT][4];  // QR 8: [2], [3] for the remainders
+  float acc[NT][4];   // QR 8: [2], [3] for the remainders
   float rest[NT][4];  // QR 16: the remainders'
-  float m[RV], l[RV], lag;
+  float m[RV], l[RV], down;
 
   __device__ __forceinline__ void init(char*) {}
   __device__ __forceinline__ void begin(const char* q, int rows, int tiles, int lane) {
-    lag = pat_above(tiles) - 8.f;
+    down = pat_exp2i(-pat_above(tiles));
     const uint32_t qs = smem_u32(q);
     // rows 0..7 (and 8..15) of Q as first-operand fragments; rows that do not exist repeat row 0
     // and are not written
@@ -525,12 +522,12 @@ struct PatWarp<bf16, HD, QR> {
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
       t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
       mx[r] = t;
-      move |= t + lag > m[r];
+      move |= t > m[r] + 8.f;
     }
     if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
       for (int r = 0; r < RV; ++r) {
-        const float mn = fmaxf(m[r], mx[r] + (lag + 8.f));
+        const float mn = fmaxf(m[r], mx[r]);
         const float f = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
         m[r] = mn;
         l[r] *= f;
@@ -553,7 +550,7 @@ struct PatWarp<bf16, HD, QR> {
     for (int r = 0; r < RV; ++r) {
       const float ref = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[r][i] = ex2_fast(p[r][i] - ref);
+      for (int i = 0; i < 4; ++i) p[r][i] = ex2_fast(p[r][i] - ref) * down;
       l[r] += (p[r][0] + p[r][1]) + (p[r][2] + p[r][3]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -612,7 +609,7 @@ struct PatWarp<float, HD, QR> {
   using S = PatShape<float, HD, QR>;
   static constexpr int CPR = HD / 4, E = HD / 32;
   float acc[QR][E];
-  float m[QR], l[QR], lag;
+  float m[QR], l[QR], down;
   float4* qb;  // [QR][CPR]
   float* wb;   // [QR][PAT_TILE]
 
@@ -621,7 +618,7 @@ struct PatWarp<float, HD, QR> {
     wb = reinterpret_cast<float*>(side + QR * HD * 4);
   }
   __device__ __forceinline__ void begin(const char* qs, int rows, int tiles, int lane) {
-    lag = pat_above(tiles) - 8.f;
+    down = pat_exp2i(-pat_above(tiles));
     // the stage is refilled before the item ends
     const float4* from = reinterpret_cast<const float4*>(qs);
     for (int i = lane; i < QR * CPR; i += 32)
@@ -658,8 +655,8 @@ struct PatWarp<float, HD, QR> {
       s[r] = seen ? s[r] * scale_log2 : -INFINITY;
       // as above, the maximum moves only when a score exceeds it by more than 8; most tiles need
       // one vote per row and no reduction
-      if (__any_sync(0xffffffffu, s[r] + lag > m[r])) {
-        float t = fmaxf(m[r], s[r] + (lag + 8.f));
+      if (__any_sync(0xffffffffu, s[r] > m[r] + 8.f)) {
+        float t = fmaxf(m[r], s[r]);
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
         const float f = exp2f(m[r] - t);
@@ -668,7 +665,7 @@ struct PatWarp<float, HD, QR> {
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[r][e] *= f;
       }
-      const float p = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+      const float p = exp2f(s[r] - (m[r] == -INFINITY ? 0.f : m[r])) * down;
       l[r] += p;
       if (half == 0) wb[r * PAT_TILE + key] = p;
     }
@@ -725,7 +722,7 @@ struct PatOut {
   float* part;  // row 0 of the piece
   float2* ml;
   int hd;
-  float above;
+  int above;
   __device__ __forceinline__ float stat(int row, float m, float l, bool first) const {
     if (!out) {
       if (first) ml[row] = make_float2(m, l);
