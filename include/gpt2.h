@@ -489,8 +489,9 @@ int gpt2_op_paged_kv_append(const gpt2_paged_kv* kv, const gpt2_paged_rows* rows
  * are all t < L (window 0) or the newest `window` and the first `sinks` of them (window > 0).
  * q and out: rows of n_q_heads heads of head_dim contiguous elements, row strides ldq and ldo;
  * f32_lse (nullable): [n_seqs][n_q_heads], the natural logarithm of the sum of exponentials.
- * L = 0 gives out = 0 and lse = -inf. A length outside [0, max_pages*page_size] is brought to
- * the nearer end, a key whose page id is bad is left out, and both raise the status word.
+ * L = 0 gives out = 0 and lse = -inf. The lengths must not change while the call runs. A length
+ * outside [0, max_pages*page_size] is brought to the nearer end, a key whose page id is bad is
+ * left out, and both set bit 0 of the status word.
  * Softmax statistics and sums are fp32, each output is rounded once; a NaN in q, or in a
  * visible key or value, gives NaN where the formula does, one in an unseen place has no effect.
  * An infinite visible value gives its element that infinity (NaN beside one of the other sign;

@@ -89,8 +89,9 @@ __device__ __forceinline__ uint4 pkv_pack(const float (&f)[4], float) {
 // q_out may be q. Bound by HBM: the row is read and written once. A thread reads its vectors
 // before it looks up where they go (position, then page, then the table row): the two latencies
 // overlap. The grid fills every SM once (a grid of many short blocks spent a fifth of the time
-// on starting them), so 32 registers a thread are allowed. 16,384 rows of 12 + 12 + 12 heads of
-// 64 in bf16, 151 MB moved: 27.8 us, 5.4 TB/s (a plain copy of as many bytes: 24.6 us).
+// on starting them), so 32 registers a thread are allowed (rotated halves in bf16 spill 20 bytes
+// for it). 16,384 rows of 12 + 12 + 12 heads of 64 in bf16, 151 MB moved: 28.0 us, 5.4 TB/s (a
+// plain copy of as many bytes: 24.6 us).
 template <class T, bool PAIRS>
 __global__ void __launch_bounds__(PKV_THREADS, PKV_BLOCKS) paged_append_kernel(const PagedAppendArgs a) {
   constexpr int VN = 16 / sizeof(T);
@@ -234,10 +235,10 @@ __device__ __forceinline__ float pat_lse(const PagedAttnArgs& a, float m, float 
 // that it was the instructions of a warp: two or three warps per scheduler, each a chain of
 // dependent steps, of which 16-byte copies by all lanes were half (300 us). Shorter ones: the
 // chain of lengths, place, page, copy, first tile (3.5 us) and, when items cross blocks, arrival
-// and join (3 to 4 us): 16 sequences of 1,024 tokens, 12 heads of 64 (50 MB) take 16.3 us, of
-// which 7 us stream; one of 100 tokens 5.4 us.
+// and join (3 to 4 us): 16 sequences of 1,024 tokens, 12 heads of 64 (50 MB) take 16.5 us, of
+// which 7 us stream; one of 100 tokens 5.5 us.
 // Pages that keep each head's tokens together read faster than pages of whole tokens, whose rows
-// of 128 bytes are far apart (12 and 25 heads of 64: 94 % against 85 and 77 % of the copy rate).
+// of 128 bytes are far apart (12 and 25 heads of 64: 94 % against 86 and 76 % of the copy rate).
 constexpr int PAT_MAX_BLOCKS = 256;
 constexpr int PAT_SMEM = 226 * 1024;  // of a block
 
@@ -273,7 +274,13 @@ struct PatShape {
     const int fit = (PAT_SMEM - 1024 - (n_seqs + 1) * 4) / warp_bytes(rows);
     return fit >= 12 ? 12 : fit >= 8 ? 8 : fit;
   }
-  // an item of at most so many tiles (128 KB of keys and values) is not split between blocks
+  // an item of at most so many tiles (128 KB of keys and values) is not split between blocks.
+  // Splitting never, or always, against this (1 to 128 sequences of 64 to 8,192 tokens, heads of
+  // 32, 64 and 128): one sequence of 256 tokens, 12 heads of 64, 8.3 us split and 6.5 whole, of 512
+  // 8.1 and 7.8, of 1,024 8.5 and 10.6. Of 158 such cases the rule is within 3 % of the better side
+  // in 129, behind it by up to 13 % (0.2 to 0.8 us) where sequences of up to 128 tokens need no
+  // join either way, and by up to 19 % (2.4 us) where 16 sequences of 1,024 to 2,048 tokens, whole,
+  // would leave just a few SMs idle (8 heads of 128, 16 of 32).
   static constexpr int WHOLE = 131072 / (2 * TILE);
   static constexpr int smem(int rows, int n_seqs) {
     return 1024 + warps(rows, n_seqs) * warp_bytes(rows) + (n_seqs + 1) * 4;
@@ -431,9 +438,9 @@ struct PatWarp;
 // first operand's fragment. The weights are not rounded to one bf16: with up to 8 query heads
 // (QR 8) rows 8..15 of the operand, otherwise empty, hold the remainders p - bf16(p), and the
 // two halves of the result are added at the end; with up to 16 heads the remainders take a
-// second product and sums of their own. P is so carried to 2^-16 of its value at no or little
-// cost (the products are far from the tensor cores' rate: the kernel is bound by reading the
-// cache). A remainder may be 0 or negative, and its product with an infinite value NaN or of the
+// second product and sums of their own. P is so carried to 2^-16 of its value, with up to 8 heads
+// at no cost (the products are far from the tensor cores' rate: the kernel is bound by reading the
+// cache; 12 and 16 heads run at 71 and 58 % of the copy rate, bound by a warp's instructions). A remainder may be 0 or negative, and its product with an infinite value NaN or of the
 // other sign; where the first half is infinite or NaN, it is the result.
 // The running maximum moves only when a tile exceeds it by more than 8 (weights and sums against
 // an older maximum are at most 2^8 larger, and as exact), so most tiles do not rescale the output.
@@ -601,9 +608,9 @@ struct PatWarp<bf16, HD, QR> {
 
 // fp32: fp32 products and sums. Scores: a lane has a key and half of the elements; weights go
 // to the P V loop through shared memory, where a lane holds HD/32 output elements (neighbours,
-// or 32 apart for HD 96). One query head per key head is bound by HBM (12 heads of 64: 92 % of
-// the copy rate); with 4 and 8 the shared-memory reads of queries and weights bound it (62 % and
-// 44 %; packed pairs of fp32 products were slower for the moves they need).
+// or 32 apart for HD 96). One query head per key head is bound by HBM (12 heads of 64: 91 % of
+// the copy rate); with 4 and 8 the shared-memory reads of queries and weights bound it (63 % and
+// 45 %; packed pairs of fp32 products were slower for the moves they need).
 template <int HD, int QR>
 struct PatWarp<float, HD, QR> {
   using S = PatShape<float, HD, QR>;
