@@ -464,9 +464,9 @@ typedef struct {
  * rounded once; elements from rot_dim on are copied. q (nullable, with q_out and n_q_heads):
  * query rows of the same tokens, rotated the same way into q_out (may be q itself, with the
  * same row stride; GPT2_ERR_CONFIG when its rows overlap those of q, k or v otherwise; it may not
- * overlap the cache either). A row whose position, sequence, table entry or
- * rotation row is outside its range is skipped and raises the status word; rows that are skipped
- * leave q_out as it was. Rows must name distinct slots: of two rows for one slot, each 16 bytes
+ * overlap the cache either). A row whose position, sequence, table entry or rotation row is outside
+ * its range is skipped and sets bit 0 of the status word; rows that are skipped leave q_out as it
+ * was. Rows must name distinct slots: of two rows for one slot, each 16 bytes
  * come from either. The cache's strides must keep its heads apart, each stepping over what the
  * smaller ones span (GPT2_ERR_CONFIG: an expanded tensor can be read, not appended to), and k
  * and v may not share elements. Row bases and strides (elements) are multiples of 16 bytes; n_rows *

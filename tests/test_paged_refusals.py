@@ -341,6 +341,15 @@ def test_append_refuses_overlapping_query_rows(change):
     assert b"q_out" in tsb.lib().gpt2_op_last_error()
 
 
+@pytest.mark.parametrize("dtype,ld", [(tsb.FP32, 1 << 62), (tsb.BF16, 1 << 62), (tsb.FP32, (1 << 63) - 64), (tsb.BF16, (1 << 63) - 64)])
+def test_append_checks_row_strides_of_any_size(dtype, ld):
+    # strides whose bytes do not fit 64 bits
+    f = dict(k=A + (1 << 20), v=A + (2 << 20), ldq=ld, ldqo=ld)
+    assert append(cache(dtype=dtype), **f, q_out=A + 16) == CONFIG
+    assert b"q_out" in tsb.lib().gpt2_op_last_error()
+    assert append(cache(dtype=dtype), **f, q_out=A + 16, N=1) == CONFIG
+
+
 APART_CHECK = r"""
 #include <set>
 #include "paged_index.cuh"

@@ -1249,11 +1249,11 @@ inline int paged_kv_append(const LaunchCtx& c, const gpt2_paged_kv* kv, const gp
     return fail(c, GPT2_ERR_BATCH, "paged_kv_append: more than 2^30 pairs of 16-byte vectors");
   if (a.nh) {
     // q_out against the rows that other threads read
-    const int64_t es = 16 / vn, wq = a.nh * hd * es, wk = a.c.nkv * hd * es;
-    auto at = [&](const void* p) { return static_cast<const char*>(p) - static_cast<const char*>(a.q_out); };
-    if (!paged_rows_apart(a.ldqo * es, wq, at(a.q), a.ldq * es, wq, a.rows, true) ||
-        !paged_rows_apart(a.ldqo * es, wq, at(a.k), a.ldk * es, wk, a.rows, false) ||
-        !paged_rows_apart(a.ldqo * es, wq, at(a.v), a.ldv * es, wk, a.rows, false))
+    const int64_t es = 16 / vn, wq = a.nh * hd, wk = a.c.nkv * hd;
+    auto at = [&](const void* p) { return (static_cast<const char*>(p) - static_cast<const char*>(a.q_out)) / es; };
+    if (!paged_rows_apart(a.ldqo, wq, at(a.q), a.ldq, wq, a.rows, true) ||
+        !paged_rows_apart(a.ldqo, wq, at(a.k), a.ldk, wk, a.rows, false) ||
+        !paged_rows_apart(a.ldqo, wq, at(a.v), a.ldv, wk, a.rows, false))
       return fail(c, GPT2_ERR_CONFIG,
                   "paged_kv_append: q_out may be q with the same row stride, and may not overlap q, k or v otherwise");
   }

@@ -440,8 +440,9 @@ struct PatWarp;
 // two halves of the result are added at the end; with up to 16 heads the remainders take a
 // second product and sums of their own. P is so carried to 2^-16 of its value, with up to 8 heads
 // at no cost (the products are far from the tensor cores' rate: the kernel is bound by reading the
-// cache; 12 and 16 heads run at 71 and 58 % of the copy rate, bound by a warp's instructions). A remainder may be 0 or negative, and its product with an infinite value NaN or of the
-// other sign; where the first half is infinite or NaN, it is the result.
+// cache; 12 and 16 heads run at 71 and 58 % of the copy rate, bound by a warp's instructions). A
+// remainder may be 0 or negative, and its product with an infinite value NaN or of the other sign;
+// where the first half is infinite or NaN, it is the result.
 // The running maximum moves only when a tile exceeds it by more than 8 (weights and sums against
 // an older maximum are at most 2^8 larger, and as exact), so most tiles do not rescale the output.
 template <int HD, int QR>
@@ -796,8 +797,8 @@ struct PatSum {
 // `rounds` rounds; `scratch` has 24 bytes per thread.
 constexpr int PAJ_AHEAD = 8;
 template <class T, int HD>
-__device__ __forceinline__ void pat_join(const PagedAttnArgs& a, const PagedAttnPlan& pl, int c0, int c1, int rows, int tiles, T* out,
-                                         float* lse, char* scratch, int t, int threads, int rounds) {
+__device__ __forceinline__ void pat_join(const PagedAttnArgs& a, const PagedAttnPlan& pl, int c0, int c1, int rows, int tiles,
+                                         T* out, float* lse, char* scratch, int t, int threads, int rounds) {
   constexpr int VEC = HD / 4;
   float4* s_o = reinterpret_cast<float4*>(scratch);
   float2* s_ml = reinterpret_cast<float2*>(scratch + 16 * blockDim.x);

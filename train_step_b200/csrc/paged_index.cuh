@@ -104,8 +104,9 @@ G2_HD bool paged_next(PagedCursor& c, const int* before, int items) {
   return true;
 }
 
-// n rows of `wa` bytes at 0, lda, 2 lda ... and n of `wb` bytes at d, d + ldb ... (host): whether no
-// byte belongs to a row of each. in_place: a row may also be the other's of the same index, exactly.
+// n rows of `wa` elements at 0, lda, 2 lda ... and n of `wb` at d, d + ldb ... (host; 0 < wa <= lda
+// and 0 < wb <= ldb of any size): whether no element belongs to a row of each. in_place: a row may
+// also be the other's of the same index, exactly.
 inline bool paged_rows_apart(int64_t lda, int64_t wa, int64_t d, int64_t ldb, int64_t wb, int64_t n, bool in_place) {
   typedef __int128 wide;
   if (d >= (wide)lda * (n - 1) + wa || d + (wide)ldb * (n - 1) + wb <= 0) return true;
